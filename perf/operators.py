@@ -159,7 +159,6 @@ def prepare(case, seed):
             import autotuning_tcgen05_tmem_gb300 as lib
             s["packed"] = lib.wq_pack(s["codes"], s["scales"], s["z"], N, case["group"], gated=_glu(case["epi"]))
             s["plan"] = lib.wq_plan(K, N, group=case["group"], zeros=case["zeros"], epi=case["epi"])
-            s["plan"].set_independent_weights()      # a model's weights: nothing before the call writes them
             s["y"] = torch.empty(T, out, device=DEV, dtype=torch.bfloat16)
         return s
     H, I, E, k = case["H"], case["I"], case["E"], case["k"]
