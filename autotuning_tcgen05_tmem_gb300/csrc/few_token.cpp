@@ -451,7 +451,8 @@ extern "C" int gemm_moe_plan(const gemm_moe_desc *desc, gemm_moe_plan_t *out)
     p->h_rows = pairs + 64;   // a box of rows may reach past the last one
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     const size_t n_logits = up((size_t)kMoeMaxSlices * d.max_tokens * d.experts * 4),
-                 n_ids = up((size_t)pairs * 4), n_h = up((size_t)p->h_rows * d.inter * 2),
+                 n_ids = up((size_t)pairs * 4),
+                 n_h = up((size_t)p->h_rows * d.inter * (d.weights == GEMM_MOE_BF16 ? 4 : 2)),
                  n_part = up((size_t)q.sm_count * 2 * tiles_of_tokens(d.max_tokens) * 8 * kFtTileRows * 4);
     e = cudaMalloc(&p->ctl, p->ctl_bytes);
     if (e == cudaSuccess) e = cudaMemset(p->ctl, 0, p->ctl_bytes);
@@ -538,14 +539,14 @@ static int moe_run(gemm_moe_plan_t p, int64_t tokens, const void *x, const void 
     k.route_reduce = tokens > 8;
     k.max_tiles_up = (int32_t)p->max_tiles_up;
 
-    // Tables of the routing need about 14 KB.
+    // Tables of the routing need about 13 KB.
     constexpr uint32_t kTables = 16 * 1024;
-    static_assert(kMoeMaxExperts * 20 + kMoeMaxPairs * 5 + 16 <= (int)kTables, "routing tables");
+    static_assert(kMoeMaxExperts * 20 + kMoeMaxPairs * 5 + kMoeMaxRuns * 8 + 64 <= (int)kTables, "routing tables");
     const uint32_t red = red_bytes(wq ? FT_MOE_W4 : FT_MOE_BF16, nt), acc = (uint32_t)k.t8 * (kFtTileRows + 4) * 4u;
     k.off_route = kFtCtl;
     k.off_ring = kFtCtl + kTables;
     k.off_x = wq ? round_up(4u * (uint32_t)k.chunk_bytes, 1024) : (uint32_t)step_k * 256u;
-    k.off_meta = k.off_x + (uint32_t)k.t8 * (uint32_t)step_k * 2u;
+    k.off_meta = k.off_x + (uint32_t)(moe_stage_rows(wq ? FT_MOE_W4 : FT_MOE_BF16, k.t8) * step_k * 2);
     k.stage_bytes = wq ? round_up(k.off_meta + meta_bytes(k.t8), 1024) : k.off_meta;
     static_assert(8 * (2 * kMoeMaxExperts + 2 * kMoeMaxTopK) * 4 <= kRouteWeightBytes, "a token group's choice");
     const int64_t room = p->smem_limit - 1024 - k.off_ring - red - acc;
@@ -577,6 +578,7 @@ static int moe_run(gemm_moe_plan_t p, int64_t tokens, const void *x, const void 
     k.ids = p->ids;
     k.weights = p->weights;
     k.h = p->h;
+    k.h_rows = (int32_t)p->h_rows;
     k.partials = p->partials;
     k.ctl = p->ctl;
     k.timeout_ns = g_timeout_ns.load();
@@ -591,7 +593,7 @@ static int moe_run(gemm_moe_plan_t p, int64_t tokens, const void *x, const void 
     rc = wq ? encode_rows(&m.x, x, d.hidden, tokens, (int)tokens) : encode_tokens(&m.x, x, d.hidden, tokens, k.t8, step_k / 64);
     for (int i = 0; i < 4 && !rc && (1 << i) <= nt; ++i)
         rc = wq ? encode_rows(&m.h[i], p->h, d.inter, p->h_rows, 8 << i)
-                : encode_tokens(&m.h[i], p->h, d.inter, p->h_rows, 8 << i, step_k / 64);
+                : encode_tokens(&m.h[i], p->h, d.inter, 2 * p->h_rows, 8 << i, step_k / 64);
     if (!rc && !wq) {
         rc = encode_stack(&m.gate_up, gate_up, (uint64_t)d.inter * 2, (uint64_t)d.hidden, (uint64_t)d.experts,
                           (uint32_t)step_k, 2);

@@ -505,9 +505,10 @@ __device__ __forceinline__ void ft_scale_w4(Acc<NW> &acc)
 // piece of the row-major weight with 128-byte swizzled rows.  `mh` picks the
 // warp's 32 columns: plain, columns 32·mh + 16·m + row; gated (32 gate columns,
 // then 32 up), features 16·mh + 8·m + g with the gate in the fragment's rows g
-// and the up in rows g + 8.  xbox: the tokens' 64 K that hold k0.
+// and the up in rows g + 8.  xbox: the tokens' 64 K that hold k0; xlow: those of
+// their second bf16 part (kept h, down phase), 0 where they have one part.
 template <int NT>
-__device__ __forceinline__ void ft_box_bf16(uint32_t box, int mh, int k0, bool gated, uint32_t xbox,
+__device__ __forceinline__ void ft_box_bf16(uint32_t box, int mh, int k0, bool gated, uint32_t xbox, uint32_t xlow,
                                             const uint32_t (&xrow)[NT], int lane, Acc<NT> &acc)
 {
     uint32_t a[2][2][4];
@@ -521,16 +522,20 @@ __device__ __forceinline__ void ft_box_bf16(uint32_t box, int mh, int k0, bool g
             ldmatrix_x4_trans(box + krow * 128u + ((ck ^ (krow & 7u)) << 4), a[m][ks]);
         }
     const uint32_t cx = (uint32_t)((k0 & 32) / 8 + (lane >> 3));
+    auto multiply = [&](uint32_t box_of_tokens) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        uint32_t b[4];
-        ldmatrix_x4(xbox + xrow[n] * 128u + ((cx ^ (xrow[n] & 7u)) << 4), b);
+        for (int n = 0; n < NT; ++n) {
+            uint32_t b[4];
+            ldmatrix_x4(box_of_tokens + xrow[n] * 128u + ((cx ^ (xrow[n] & 7u)) << 4), b);
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-            mma_bf16(acc.v[m][n], a[m][0][0], a[m][0][1], a[m][0][2], a[m][0][3], b[0], b[1]);
-            mma_bf16(acc.v[m][n], a[m][1][0], a[m][1][1], a[m][1][2], a[m][1][3], b[2], b[3]);
+            for (int m = 0; m < 2; ++m) {
+                mma_bf16(acc.v[m][n], a[m][0][0], a[m][0][1], a[m][0][2], a[m][0][3], b[0], b[1]);
+                mma_bf16(acc.v[m][n], a[m][1][0], a[m][1][1], a[m][1][2], a[m][1][3], b[2], b[3]);
+            }
         }
-    }
+    };
+    multiply(xbox);
+    if (xlow) multiply(xlow);
 }
 
 // --- Sums across the warps of a CTA ------------------------------------------------

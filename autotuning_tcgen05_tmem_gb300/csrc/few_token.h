@@ -175,7 +175,9 @@ struct MoeParams {
     float *logits;                     // [slices][T][E] partial router products
     int32_t *ids;                      // [T][top_k]
     float *weights;
-    void *h;                           // [T·top_k (+ padding)][I] activations, by expert
+    void *h;                           // [T·top_k (+ padding)][I] activations, by expert; bf16
+                                       // experts: high parts, then (h_rows rows on) low parts
+    int32_t h_rows;
     float *partials;                   // two tiles for each CTA
     int32_t *ctl;                      // [0] status, [2..3] arrivals (64-bit), [8..15] router groups,
                                        // [16..] tile counters of the up and the down phase
@@ -189,6 +191,7 @@ constexpr int kMoeMaxSlices = 32;            // of H, in the router product
 constexpr int kRouteWeightBytes = 32 * 1024; // of the router weight, staged at once,
 constexpr int kRouteRows = 512;              // and at most so many of its rows
 constexpr int kMoeMaxPairs = kFtMaxTokens * kMoeMaxTopK;
+constexpr int kMoeMaxRuns = kMoeMaxExperts + kMoeMaxPairs / 32;   // of a down tile
 
 struct WqPrepareParams {
     const void *x;
@@ -215,8 +218,20 @@ struct MoeMaps {
     CUtensorMap x, gate_up, down, h[4];
 };
 // K of one bf16 step (1 token, 2 of 8 experts of 4096x14336: 120.5 us, 122.6 with 64);
-// above 32 tokens a step of 128 would leave the ring two slots.
-constexpr int moe_step_k(int nt) { return nt <= 4 ? 128 : 64; }
+// above 16 tokens a step of 128, with both parts of h, would leave the ring two slots.
+__host__ __device__ constexpr int moe_step_k(int nt) { return nt <= 2 ? 128 : 64; }
+// Tokens of an expert that one run of the down phase takes.  bf16 experts read two parts
+// of each row of h: with more than 32 tokens at once a stage would hold 16 KB of h beside
+// 16 KB of weights and the ring three slots instead of four (64 tokens, 4 of 32 experts of
+// 4096x2048: 336 us, 303 so); an expert with more has its down weights read twice instead.
+constexpr int kMoeDownTokens = 32;
+__host__ __device__ constexpr int moe_down_tokens(int kernel) { return kernel == FT_MOE_BF16 ? kMoeDownTokens : kFtMaxTokens; }
+// Rows of a stage's tokens, in rows of step_k bf16.
+__host__ __device__ constexpr int moe_stage_rows(int kernel, int t8)
+{
+    return kernel != FT_MOE_BF16 || t8 > kMoeDownTokens ? t8 : 2 * t8;
+}
+static_assert(moe_stage_rows(FT_MOE_BF16, kFtMaxTokens) >= 2 * kMoeDownTokens, "both parts of h");
 cudaError_t moe_set_smem_limit(int bytes);
 cudaError_t launch_moe(int nt, int wq, const MoeMaps &m, const MoeParams &p, int grid, int smem, cudaStream_t stream);
 

@@ -6,7 +6,7 @@
 //
 // Bound by the weights of the experts that were chosen, each read once however
 // many tokens chose it: 1 token, 2 of 8 bf16 experts of 4096x14336, 119 us, 5.9 TB/s (87%
-// of a copy); 64 tokens, 4 of 32 of 4096x2048, 285 us, 5.7 TB/s; 16 tokens, 8 of 64 4-bit
+// of a copy); 64 tokens, 4 of 32 of 4096x2048, 303 us, 5.3 TB/s; 16 tokens, 8 of 64 4-bit
 // experts, 187 us, 4.0 TB/s (the multiplications and conversions of 4-bit steps, not the
 // memory, bound that one).  Small layers are bound by the chain of phases: 1 token, 8 of
 // 64 of 2048x1024, takes 38 us for 15 us of weights.  One cooperative launch, one CTA to
@@ -43,10 +43,13 @@ struct RouteTables {
     int32_t offset[kMoeMaxExperts];            // first of its rows in h
     int32_t act_expert[kMoeMaxExperts];        // experts chosen by any token, ascending
     int32_t act_count[kMoeMaxExperts];
+    // The down phase's runs of a tile: an expert's rows, at most moe_down_tokens of them.
+    int32_t down_expert[kMoeMaxRuns];
+    uint16_t down_offset[kMoeMaxRuns], down_count[kMoeMaxRuns];
     float weight[kMoeMaxPairs];                // by row of h
     uint8_t token[kMoeMaxPairs];
     FtShare up, down;                          // how the two phases divide
-    int32_t n_active;
+    int32_t n_active, n_down;
     int32_t last;                              // this CTA's slice was the last of its token group
 };
 
@@ -299,7 +302,7 @@ __device__ __forceinline__ void choose(const MoeParams &p, float *logits, int32_
 // Tables of the chosen experts, from ids and weights in shared memory.  An id
 // outside [0, E) is an empty place; a second mention of an expert by the same
 // token adds its weight to the first.
-template <int W>
+template <int W, int DOWN>
 __device__ __forceinline__ void build_tables(const MoeParams &p, RouteTables *rt, const int32_t *ids, const float *wts,
                                              int tid)
 {
@@ -312,31 +315,40 @@ __device__ __forceinline__ void build_tables(const MoeParams &p, RouteTables *rt
     }
     named_bar_sync(1, W);
     if (tid < 32) {
-        int rows = 0, active = 0;
+        int rows = 0, active = 0, runs = 0;
         for (int e0 = 0; e0 < p.E; e0 += 32) {
             const int e = e0 + tid;
             const int n = e < p.E ? __popcll(rt->mask[e]) : 0;
-            int incl = n;
+            const int parts = (n + DOWN - 1) / DOWN;
+            int incl = n | parts << 16;            // rows and runs before, side by side
 #pragma unroll
             for (int o = 1; o < 32; o *= 2) {
                 const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
                 if (tid >= o) incl += v;
             }
+            const int first = rows + (incl & 0xFFFF) - n;
             const uint32_t used = __ballot_sync(0xFFFFFFFFu, n > 0);
-            if (e < p.E) rt->offset[e] = rows + incl - n;
+            if (e < p.E) rt->offset[e] = first;
+            for (int i = 0; i < parts; ++i) {
+                const int a = runs + (incl >> 16) - parts + i;
+                rt->down_expert[a] = e;
+                rt->down_offset[a] = (uint16_t)(first + i * DOWN);
+                rt->down_count[a] = (uint16_t)min(DOWN, n - i * DOWN);
+            }
             if (n > 0) {
                 const int a = active + __popc(used & ((1u << tid) - 1u));
                 rt->act_expert[a] = e;
                 rt->act_count[a] = n;
             }
-            rows += __shfl_sync(0xFFFFFFFFu, incl, 31);
+            const int all = __shfl_sync(0xFFFFFFFFu, incl, 31);
+            rows += all & 0xFFFF, runs += all >> 16;
             active += __popc(used);
         }
         if (tid == 0) {
-            rt->n_active = active;
+            rt->n_active = active, rt->n_down = runs;
             // Step by step: even shares at staggered places of the weights.
             rt->up = ft_share_of((int64_t)active * p.tiles_up, p.nkb_up, 1, gridDim.x);
-            rt->down = ft_share_of(p.tiles_down, active * p.nkb_down, 1, gridDim.x);
+            rt->down = ft_share_of(p.tiles_down, runs * p.nkb_down, 1, gridDim.x);
         }
     }
     named_bar_sync(1, W);
@@ -358,7 +370,8 @@ __device__ __forceinline__ void build_tables(const MoeParams &p, RouteTables *rt
 }
 
 // A CTA's share of a phase as runs of steps on one tile and expert: in the up phase
-// expert by expert, tile by tile; in the down phase tile by tile, expert by expert.
+// expert by expert, tile by tile; in the down phase tile by tile, expert by expert (an
+// expert of many tokens in several runs).
 // (Divides once: a 64-bit division for every run took as long as a step.)
 struct Runs {
     int a, tile, k, left;   // place in the tables, tile, first K step; steps from here on
@@ -367,7 +380,7 @@ struct Runs {
     __device__ __forceinline__ Runs(const MoeParams &p, const RouteTables *rt, bool up_) : up(up_)
     {
         const FtShare &sh = up ? rt->up : rt->down;
-        nkb = up ? p.nkb_up : p.nkb_down, na = rt->n_active, nt = p.tiles_up;
+        nkb = up ? p.nkb_up : p.nkb_down, na = up ? rt->n_active : rt->n_down, nt = p.tiles_up;
         a = tile = k = left = 0;
         if ((int)blockIdx.x >= sh.parts) return;
         const int64_t s0 = ft_share_begin(sh, blockIdx.x), run = s0 / nkb;
@@ -376,6 +389,12 @@ struct Runs {
         a = (int)(up ? run / nt : run % na), tile = (int)(up ? run % nt : run / na);
     }
     __device__ __forceinline__ int steps() const { return min(nkb - k, left); }
+    // The run's rows of h.
+    __device__ __forceinline__ int count(const RouteTables *rt) const { return up ? rt->act_count[a] : rt->down_count[a]; }
+    __device__ __forceinline__ int offset(const RouteTables *rt) const
+    {
+        return up ? rt->offset[rt->act_expert[a]] : rt->down_offset[a];
+    }
     __device__ __forceinline__ void next()
     {
         left -= steps();
@@ -403,17 +422,17 @@ struct MoeKernel {
     static constexpr bool kAll = FMT == 1 && NTMAX > 2;
     using Walk = StepWalk<FMT == 0 ? 1 : ft_k_parts(FMT, NTMAX, 1), kAll>;
 
-    // Multiplies `n` steps of one tile on one expert of NT tiles and hands the sums
-    // over; the ring position moves on.  up: the tokens' rows are those of x, else
-    // of h.
+    // Multiplies `n` steps of one tile on n_tok tokens (NT tiles) of one expert, whose
+    // rows of h begin at `off`, and hands the sums over; the ring position moves on.
+    // up: the tokens' rows are those of x, else of h.
     template <int NT>
     static __device__ __forceinline__ void steps(const MoeParams &p, const Ring &ring, const HandOver &hand,
                                                  const WaitCtl &ctl, const RouteTables *rt, int n, Walk &walk, RingPos &h,
-                                                 bool up, int a, int chunks, uint8_t *gbase, uint32_t base, int warp, int lane)
+                                                 bool up, int n_tok, int off, int chunks, uint8_t *gbase, uint32_t base, int warp,
+                                                 int lane)
     {
         constexpr int TP = ft_token_parts(NT), KP = ft_k_parts(FMT, NTMAX, NT), NW = NT / TP;
         const int cg = warp & 3, part = (warp >> 2) % KP, tok0 = (warp >> 2) / KP * NW * 8;
-        const int n_tok = rt->act_count[a], off = rt->offset[rt->act_expert[a]];
         const uint32_t box_bytes = up ? (uint32_t)p.t8 * 128u : (uint32_t)NT * 1024u;
         uint32_t xrow[NW];
 #pragma unroll
@@ -431,8 +450,9 @@ struct MoeKernel {
 #pragma unroll
                 for (int k0 = 0; k0 < kStepK / KP; k0 += 32) {
                     const int k = part * (kStepK / KP) + k0;
-                    ft_box_bf16<NW>(st + (uint32_t)(cg >> 1) * kColBox, cg & 1, k, up, xb + (uint32_t)(k >> 6) * box_bytes,
-                                    xrow, lane, acc);
+                    const uint32_t xbox = xb + (uint32_t)(k >> 6) * box_bytes;
+                    ft_box_bf16<NW>(st + (uint32_t)(cg >> 1) * kColBox, cg & 1, k, up, xbox,
+                                    up ? 0u : xbox + (uint32_t)kBoxes * box_bytes, xrow, lane, acc);
                 }
             } else {
                 const float *const meta = reinterpret_cast<const float *>(gbase + (st - base) + p.off_meta);
@@ -461,10 +481,9 @@ struct MoeKernel {
     {
         RingPos pos;
         int first = cw;
-        auto step = [&](int a, bool up) {
+        auto step = [&](int n_tok, int off, bool up) {
             const uint32_t st = ring.stage(pos);
             float *const meta = reinterpret_cast<float *>(gbase + (st - base) + p.off_meta);
-            const int n_tok = rt->act_count[a], off = rt->offset[rt->act_expert[a]];
             ft_convert_step(ring, pos, ctl, st + p.off_x, n_tok, first, kConverters,
                             [&](int i) { return up ? (int)rt->token[off + i] : i; }, meta, p.t8, p.gpc, lane);
             first = first + 1 == kConverters ? 0 : first + 1;
@@ -472,14 +491,14 @@ struct MoeKernel {
         };
         for (int phase = 0; phase < 2; ++phase)
             for (Runs run(p, rt, phase == 0); run.left > 0; run.next())
-                for (int n = run.steps(); n > 0; --n) step(run.a, run.up);
+                for (int n = run.steps(); n > 0; --n) step(run.count(rt), run.offset(rt), run.up);
     }
 
     // The copying thread.
     static __device__ __forceinline__ void copies(const MoeMaps &m, const MoeParams &p, const Ring &ring,
                                                   const WaitCtl &ctl, const RouteTables *rt, uint64_t start, int waits)
     {
-        const int A = rt->n_active;
+        const int A = rt->n_down;
         const uint32_t box = (uint32_t)p.t8 * 128u;
         const int64_t up_bytes = (int64_t)p.ncg_up * p.nkb_up * p.chunk_bytes;
         const int64_t down_bytes = (int64_t)p.ncg_down * p.nkb_down * p.chunk_bytes;
@@ -542,19 +561,21 @@ struct MoeKernel {
                 }
             };
             auto begin = [&](const RingPos &r) {
-                const int nt = tiles_of(rt->act_count[w.a]);
-                mbar_arrive_expect_tx(ring.full(r), weight_bytes(false, w.t) + (uint32_t)(kBoxes * nt * 1024));
-                weights(false, rt->act_expert[w.a], w.t, w.kb, ring.stage(r), ring.full(r));
+                const int nt = tiles_of(rt->down_count[w.a]);
+                mbar_arrive_expect_tx(ring.full(r), weight_bytes(false, w.t) + (uint32_t)((FMT == 0 ? 2 : 1) * kBoxes * nt * 1024));
+                weights(false, rt->down_expert[w.a], w.t, w.kb, ring.stage(r), ring.full(r));
                 next(w);
             };
             auto rows_of_h = [&](const RingPos &r) {
-                const int nt = tiles_of(rt->act_count[h.a]);
+                const int nt = tiles_of(rt->down_count[h.a]);
                 const CUtensorMap *hm = nt == 1 ? &m.h[0] : nt == 2 ? &m.h[1] : nt == 4 ? &m.h[2] : &m.h[3];
-                const int row = rt->offset[rt->act_expert[h.a]];
-                if constexpr (FMT == 0)
-                    load_tokens(ring.stage(r) + p.off_x, hm, ring.full(r), h.kb * kBoxes, kBoxes, row,
-                                (uint32_t)nt * 1024u, p.h_spans);
-                else tma_load_2d(ring.stage(r) + p.off_x, hm, ring.full(r), h.kb * kWqChunkK, row);
+                const int row = rt->down_offset[h.a];
+                if constexpr (FMT == 0) {
+                    const uint32_t box = (uint32_t)nt * 1024u;
+                    for (uint32_t part = 0; part < 2; ++part)
+                        load_tokens(ring.stage(r) + p.off_x + part * kBoxes * box, hm, ring.full(r), h.kb * kBoxes, kBoxes,
+                                    row + (int)part * p.h_rows, box, p.h_spans);
+                } else tma_load_2d(ring.stage(r) + p.off_x, hm, ring.full(r), h.kb * kWqChunkK, row);
                 next(h);
             };
             const int n = (int)(s1 - s0);
@@ -603,8 +624,9 @@ struct MoeKernel {
         for (int phase = 0; phase < 2; ++phase)
             for (Runs run(p, rt, phase == 0); run.left > 0; run.next()) {
                 const int chunks = min(4, (run.up ? p.ncg_up : p.ncg_down) - 4 * run.tile);
-                with_tiles(tiles_of(rt->act_count[run.a]), [&](auto nt) {
-                    steps<decltype(nt)::value>(p, ring, hand, ctl, rt, run.steps(), walk, h, run.up, run.a, chunks, gbase, base,
+                const int n_tok = run.count(rt), off = run.offset(rt);
+                with_tiles(tiles_of(n_tok), [&](auto nt) {
+                    steps<decltype(nt)::value>(p, ring, hand, ctl, rt, run.steps(), walk, h, run.up, n_tok, off, chunks, gbase, base,
                                                warp, lane);
                 });
             }
@@ -614,7 +636,7 @@ struct MoeKernel {
     static __device__ __forceinline__ void finish(const MoeParams &p, const HandOver &hand, const WaitCtl &ctl,
                                                   const RouteTables *rt, float *yacc, volatile int32_t *flags, int tid)
     {
-        const int lane = tid & 31, A = rt->n_active;
+        const int lane = tid & 31, A = rt->n_down;
         RingPos h;
         // The sums of one expert's n_tok tokens, K parts added up.
         auto take = [&](int n_tok) {
@@ -624,7 +646,7 @@ struct MoeKernel {
             return ft_take_over(mine, h, ctl, ft_k_parts(FMT, NTMAX, nt), n_tok, tid);
         };
         for (Runs run(p, rt, true); run.left > 0; run.next()) {
-            const int n_tok = rt->act_count[run.a], off = rt->offset[rt->act_expert[run.a]], j = run.tile;
+            const int n_tok = run.count(rt), off = run.offset(rt), j = run.tile;
             float *const red = take(n_tok);
             bool last = true;
             if (run.steps() < p.nkb_up) {
@@ -634,15 +656,24 @@ struct MoeKernel {
                 last = ft_exchange(p.partials, p.t8, red, n_tok, run.k == 0, p.ctl + kMoeCtlHead + tile, first, pieces, flags + 1,
                                    tid);
             }
-            // h is rounded to bf16, the type the down product reads: its rounding
-            // errors are independent over the I features that product adds.
+            // The down product reads h in bf16.  bf16 experts: as a sum of two parts, 16
+            // significant bits together.  One part, 8 bits, would add as much error to
+            // y as its own rounding does; the second doubles only the products of h.
             __nv_bfloat16 *const hs = static_cast<__nv_bfloat16 *>(p.h);
             if (last)
                 for (int e = tid; e < 64 * n_tok; e += kFtStorers) {
                     const int f = e & 63, t = e >> 6, col = j * 64 + f;
                     if (col >= p.I) continue;
                     const float *const at = red + t * kFtRowStride + ft_gate_row(f);
-                    hs[(int64_t)(off + t) * p.I + col] = __float2bfloat16_rn(ft_act(at[0], p.act) * at[8]);
+                    const float v = ft_act(at[0], p.act) * at[8];
+                    if constexpr (FMT == 0) {
+                        const __nv_bfloat16 high = __float2bfloat16_rz(v);   // (a finite one stays finite)
+                        hs[(int64_t)(off + t) * p.I + col] = high;
+                        hs[(int64_t)(p.h_rows + off + t) * p.I + col] =
+                            __float2bfloat16_rn(isinf(v) ? 0.0f : v - __bfloat162float(high));
+                    } else {
+                        hs[(int64_t)(off + t) * p.I + col] = __float2bfloat16_rn(v);
+                    }
                 }
             ft_give_back(hand, h, lane);
         }
@@ -664,7 +695,7 @@ struct MoeKernel {
             bool whole = head;
             for (int e = tid; e < p.t8 * kFtRowStride; e += kFtStorers) yacc[e] = 0.0f;   // take's barrier comes before its use
             for (; run.left > 0 && run.tile == tile; run.next()) {
-                const int n_tok = rt->act_count[run.a], off = rt->offset[rt->act_expert[run.a]];
+                const int n_tok = run.count(rt), off = run.offset(rt);
                 whole &= run.steps() == p.nkb_down && (run.a + 1 == A || run.left > run.steps());
                 const float *const red = take(n_tok);
                 for (int e = tid; e < kFtTileRows * n_tok; e += kFtStorers) {
@@ -751,7 +782,7 @@ __global__ void __launch_bounds__(ft_threads(FMT, NTMAX), 1)
         __syncthreads();
     }
     if (warp < K::kWorkers / 32) choose<K::kWorkers>(p, logits, ids, weights, threadIdx.x);
-    if (warp < K::kWorkers / 32) build_tables<K::kWorkers>(p, rt, ids, weights, threadIdx.x);
+    if (warp < K::kWorkers / 32) build_tables<K::kWorkers, moe_down_tokens(FMT)>(p, rt, ids, weights, threadIdx.x);
     // The router's scratch in the ring was written by plain stores.
     fence_proxy_async_smem();
     __syncthreads();

@@ -671,7 +671,8 @@ void gemm_wq_plan_destroy(gemm_wq_plan_t plan);
  *   l = x · router (fp32), p = softmax(l), the top_k experts by l of each token
  *   (the lowest index among equals; NaN above all), w_j = p_j, or p_j / Σ p_j
  *   over the chosen when `normalize`;
- *   h_e = act(x · Gate_e) ⊙ (x · Up_e), rounded to bf16;
+ *   h_e = act(x · Gate_e) ⊙ (x · Up_e), held in 16 significant bits with bf16
+ *         experts, rounded to bf16 with packed ones;
  *   y = Σ_j w_j · (h_{e_j} · Down_{e_j}) (+ R).
  * router is bf16 [hidden, experts]; gate_up [experts, hidden, 2·inter] with 32
  * gate and 32 up columns in turn; down [experts, inter, hidden]: bf16, or
