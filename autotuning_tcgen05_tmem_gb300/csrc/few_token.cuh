@@ -357,15 +357,13 @@ __device__ __forceinline__ void ft_convert_rows(uint32_t x, const int (&r)[R], c
 
 // A converting warp's part of a step: of the token columns 0..n_tok-1, whose rows
 // row(i) gives, every `warps`-th from `first` on (`first` changes from step to step,
-// so that few tokens keep all warps busy).  Warps without a token only wait, which
-// keeps every warp within a lap of the ring; the one with the first token arrives
-// for them.
+// so that few tokens keep all warps busy).  A warp without a token waits and arrives
+// like the others: its arrival is what holds the slot until it has seen this lap.
 template <typename F>
 __device__ __forceinline__ void ft_convert_step(const Ring &ring, const RingPos &pos, const WaitCtl &ctl, uint32_t x, int n_tok,
                                                 int first, int warps, F row, float *meta, int t8, int gpc, int lane)
 {
     ring.wait_full(pos, ctl);
-    if (first >= n_tok) return;
     int i = first;
     for (; i + warps < n_tok; i += 3 * warps) {
         const int c[3] = {i, i + warps, min(i + 2 * warps, n_tok - 1)};
@@ -378,10 +376,7 @@ __device__ __forceinline__ void ft_convert_step(const Ring &ring, const RingPos 
     }
     fence_proxy_async_smem();   // the slot's next copy writes what plain stores wrote here
     __syncwarp();
-    if (lane == 0) {
-        const uint32_t count = first == 0 ? (uint32_t)(warps - min(warps, n_tok) + 1) : 1u;
-        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(ring.ready(pos)), "r"(count) : "memory");
-    }
+    if (lane == 0) mbar_arrive(ring.ready(pos));
 }
 
 // acc += scale · Σ (code - zero) · x · 2^-24 over a chunk's 32 columns and 256 K in
