@@ -630,6 +630,15 @@ def _operand(t, name, dtype, shape):
     return t.data_ptr()
 
 
+def _packed_operand(t, name, nbytes):
+    """Data pointer of a dense uint8 CUDA tensor of at least nbytes."""
+    import torch
+    if t.dtype != torch.uint8 or t.numel() < nbytes or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name} must be a contiguous uint8 CUDA tensor of at least {nbytes} bytes, not {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}, contiguous: {t.is_contiguous()}")
+    return t.data_ptr()
+
+
 def _groups(K: int, group: int) -> int:
     return -(-K // group) if group > 0 else 1
 
@@ -663,9 +672,8 @@ def wq_pack(codes, scales, zeros, N: int, group: int = 128, gated: bool = False,
     n = int(lib().gemm_wq_packed_bytes(mats, K, N, group, 1 if z is not None else 0))
     if out is None:
         out = torch.empty(max(n, 16), dtype=torch.uint8, device=codes.device)
-    elif out.dtype != torch.uint8 or out.numel() < n or not out.is_contiguous():
-        raise ValueError(f"out must be a contiguous uint8 tensor of at least {n} bytes")
-    _check(lib().gemm_wq_pack(c, s, z, mats, K, N, group, 1 if gated else 0, out.data_ptr(), _stream_handle(stream)))
+    _check(lib().gemm_wq_pack(c, s, z, mats, K, N, group, 1 if gated else 0, _packed_operand(out, "out", n),
+                              _stream_handle(stream)))
     return out
 
 
@@ -718,9 +726,8 @@ class WqPlan(_FewTokenPlan):
         import torch
         bf16 = torch.bfloat16
         T = x.shape[0]
-        if packed.numel() < self.packed_bytes:
-            raise ValueError(f"packed has {packed.numel()} bytes, the plan's weight needs {self.packed_bytes}")
-        _check(lib().gemm_wq_run(self._h, T, _operand(x, "x", bf16, (T, self.K)), packed.data_ptr(),
+        w = _packed_operand(packed, "packed", self.packed_bytes)
+        _check(lib().gemm_wq_run(self._h, T, _operand(x, "x", bf16, (T, self.K)), w,
                                  _operand(bias, "bias", bf16, (self.N,)),
                                  _operand(residual, "residual", bf16, (T, self.out)),
                                  _operand(y, "y", bf16, (T, self.out)), _stream_handle(stream)))
@@ -755,10 +762,7 @@ class MoePlan(_FewTokenPlan):
         import torch
         d = self.desc
         if d.weights:
-            for t, n, name in ((gate_up, self._packed[0], "gate_up"), (down, self._packed[1], "down")):
-                if t.dtype != torch.uint8 or t.numel() < n or not t.is_cuda:
-                    raise ValueError(f"{name} must be a packed CUDA weight of {n} bytes")
-            return gate_up.data_ptr(), down.data_ptr()
+            return (_packed_operand(gate_up, "gate_up", self._packed[0]), _packed_operand(down, "down", self._packed[1]))
         return (_operand(gate_up, "gate_up", torch.bfloat16, (d.experts, d.hidden, 2 * d.inter)),
                 _operand(down, "down", torch.bfloat16, (d.experts, d.inter, d.hidden)))
 
