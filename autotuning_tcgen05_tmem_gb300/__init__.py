@@ -630,12 +630,20 @@ def _operand(t, name, dtype, shape):
     return t.data_ptr()
 
 
-def _packed_operand(t, name, nbytes):
-    """Data pointer of a dense uint8 CUDA tensor of at least nbytes."""
+def _wq_layout(K, N, group, zeros, gated):
+    """What two packed weights must share to be read alike (a whole column's scale lies as one for each 256 of K)."""
+    return K, N, group or 256, bool(zeros), bool(gated)
+
+
+def _packed_operand(t, name, nbytes, layout=None):
+    """Data pointer of a dense uint8 CUDA tensor of at least nbytes; one that wq_pack wrote must have this layout."""
     import torch
     if t.dtype != torch.uint8 or t.numel() < nbytes or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{name} must be a contiguous uint8 CUDA tensor of at least {nbytes} bytes, not {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}, contiguous: {t.is_contiguous()}")
+    has = getattr(t, "wq_layout", layout)
+    if layout is not None and has != layout:
+        raise ValueError(f"{name} was packed for another layout (K, N, group, zeros, gated): {has}, not {layout}")
     return t.data_ptr()
 
 
@@ -659,7 +667,8 @@ def wq_quantize(W, group: int = 128, zeros: bool = False, stream=None):
 def wq_pack(codes, scales, zeros, N: int, group: int = 128, gated: bool = False, out=None, stream=None):
     """Pack codes [K, ceil(N/2)], scales and zero points (or None) for wq_plan and moe_plan; a leading
     expert dimension packs one weight after another.  `gated` packs a fused gate+up weight.  Returns the
-    packed uint8 tensor (allocated when `out` is None)."""
+    packed uint8 tensor (allocated when `out` is None), which remembers its layout: a plan of another one
+    refuses it."""
     import torch
     lead = tuple(codes.shape[:-2])
     mats = 1
@@ -674,6 +683,7 @@ def wq_pack(codes, scales, zeros, N: int, group: int = 128, gated: bool = False,
         out = torch.empty(max(n, 16), dtype=torch.uint8, device=codes.device)
     _check(lib().gemm_wq_pack(c, s, z, mats, K, N, group, 1 if gated else 0, _packed_operand(out, "out", n),
                               _stream_handle(stream)))
+    out.wq_layout = _wq_layout(K, N, group, z is not None, gated)   # of this tensor; its views carry none
     return out
 
 
@@ -718,7 +728,9 @@ class WqPlan(_FewTokenPlan):
     def __init__(self, handle: int, K: int, N: int, group: int, zeros: bool, epi: int, max_tokens: int):
         super().__init__(handle)
         self.K, self.N, self.group, self.zeros, self.epi, self.max_tokens = K, N, group, zeros, epi, max_tokens
-        self.out = N // 2 if EPI_BIAS_REGLU <= epi <= EPI_BIAS_SWIGLU else N
+        gated = EPI_BIAS_REGLU <= epi <= EPI_BIAS_SWIGLU
+        self.out = N // 2 if gated else N
+        self._layout = _wq_layout(K, N, group, zeros, gated)
         self.packed_bytes = int(lib().gemm_wq_packed_bytes(1, K, N, group, 1 if zeros else 0))
 
     def run(self, x, packed, bias, y, residual=None, stream=None) -> None:
@@ -726,7 +738,7 @@ class WqPlan(_FewTokenPlan):
         import torch
         bf16 = torch.bfloat16
         T = x.shape[0]
-        w = _packed_operand(packed, "packed", self.packed_bytes)
+        w = _packed_operand(packed, "packed", self.packed_bytes, self._layout)
         _check(lib().gemm_wq_run(self._h, T, _operand(x, "x", bf16, (T, self.K)), w,
                                  _operand(bias, "bias", bf16, (self.N,)),
                                  _operand(residual, "residual", bf16, (T, self.out)),
@@ -757,12 +769,15 @@ class MoePlan(_FewTokenPlan):
         if d.weights:
             self._packed = (int(lib().gemm_wq_packed_bytes(d.experts, d.hidden, 2 * d.inter, d.group, d.has_zeros)),
                             int(lib().gemm_wq_packed_bytes(d.experts, d.inter, d.hidden, d.group, d.has_zeros)))
+            self._layouts = (_wq_layout(d.hidden, 2 * d.inter, d.group, d.has_zeros, True),
+                             _wq_layout(d.inter, d.hidden, d.group, d.has_zeros, False))
 
     def _weights(self, gate_up, down):
         import torch
         d = self.desc
         if d.weights:
-            return (_packed_operand(gate_up, "gate_up", self._packed[0]), _packed_operand(down, "down", self._packed[1]))
+            return (_packed_operand(gate_up, "gate_up", self._packed[0], self._layouts[0]),
+                    _packed_operand(down, "down", self._packed[1], self._layouts[1]))
         return (_operand(gate_up, "gate_up", torch.bfloat16, (d.experts, d.hidden, 2 * d.inter)),
                 _operand(down, "down", torch.bfloat16, (d.experts, d.inter, d.hidden)))
 

@@ -88,3 +88,39 @@ def test_pack_refuses_its_output(launches, kind):
     assert launches == []
     g.wq_pack(codes, scales, None, 96, 32, out=fake(torch.zeros(n, dtype=torch.uint8)))
     assert launches == ["gemm_wq_pack"]
+
+
+def pack(K, N, group=32, zeros=False, gated=False, lead=()):
+    ng = -(-K // group) if group else 1
+    scales = fake(torch.zeros(*lead, ng, N).bfloat16())
+    z = fake(torch.zeros(*lead, ng, N, dtype=torch.uint8)) if zeros else None
+    n = int(g.lib().gemm_wq_packed_bytes(lead[0] if lead else 1, K, N, group, zeros))
+    return g.wq_pack(fake(torch.zeros(*lead, K, (N + 1) // 2, dtype=torch.uint8)), scales, z, N, group, gated=gated,
+                     out=fake(torch.zeros(n, dtype=torch.uint8)))
+
+
+def test_product_refuses_another_layout(launches):
+    """Of the same size, but its columns, groups or zero points lie elsewhere."""
+    p = g.WqPlan(0, 512, 128, 64, True, g.EPI_BIAS_SWIGLU, 4)
+    x, y, bias = fake(torch.zeros(2, 512).bfloat16()), fake(torch.zeros(2, 64).bfloat16()), fake(torch.zeros(128).bfloat16())
+    p.run(x, pack(512, 128, 64, True, True), bias, y)
+    launches.clear()
+    for other in (pack(512, 128, 64, True, False), pack(128, 512, 64, True, True), pack(512, 128, 32, True, True)):
+        assert other.numel() >= p.packed_bytes
+        with pytest.raises(ValueError, match="layout"):
+            p.run(x, other, bias, y)
+    assert "gemm_wq_run" not in launches
+    column = g.WqPlan(0, 512, 128, 0, False, g.EPI_NONE, 4)
+    column.run(x, pack(512, 128, 256), None, fake(torch.zeros(2, 128).bfloat16()))   # the same bytes as a column's scale
+    assert launches[-1] == "gemm_wq_run"
+
+
+def test_experts_refuse_another_layout(launches):
+    p = g.MoePlan(0, g.MoeDesc(64, 32, 4, 2, 8, g.MOE_WEIGHTS["wq"], 32, 0, g.EPI_BIAS_SWIGLU, 1))
+    x, router = fake(torch.zeros(2, 64).bfloat16()), fake(torch.zeros(64, 4).bfloat16())
+    gu, dn = pack(64, 64, gated=True, lead=(4,)), pack(32, 64, lead=(4,))
+    p.run(x, router, gu, dn, x)
+    for a, b, name in ((pack(64, 64, lead=(4,)), dn, "gate_up"), (gu, pack(32, 64, gated=True, lead=(4,)), "down")):
+        with pytest.raises(ValueError, match=name):
+            p.run(x, router, a, b, x)
+    assert launches.count("gemm_moe_run") == 1
