@@ -50,6 +50,14 @@ int current_device(int plan_device)
     return GEMM_OK;
 }
 
+// Zeroes device memory before it returns: the work that reads it may come on a stream
+// that does not wait for the default one, where the fill itself may have to queue.
+cudaError_t clear_memory(void *p, size_t bytes)
+{
+    cudaError_t e = cudaMemset(p, 0, bytes);
+    return e == cudaSuccess ? cudaStreamSynchronize(cudaStreamLegacy) : e;
+}
+
 // Status word of a few-token plan, after its work has finished; a part-way
 // return leaves counts behind, so the whole control block starts afresh.
 int read_word(int32_t *ctl, size_t bytes)
@@ -58,7 +66,7 @@ int read_word(int32_t *ctl, size_t bytes)
     cudaError_t e = cudaMemcpy(&st, ctl, sizeof(st), cudaMemcpyDeviceToHost);
     if (e != cudaSuccess) return cuda_err(e, "reading the status word");
     if (st == 0) return GEMM_OK;
-    e = cudaMemset(ctl, 0, bytes);
+    e = clear_memory(ctl, bytes);
     if (e != cudaSuccess) return cuda_err(e, "resetting the control block");
     return set_error(GEMM_ERR_TIMEOUT, "a device wait expired (site %d); the kernel returned early", st);
 }
@@ -246,7 +254,7 @@ extern "C" int gemm_wq_plan(int64_t K, int64_t N, int32_t group, int32_t has_zer
     p->ctl_bytes = (size_t)(1 + cdiv(N, kWqChunkCols)) * sizeof(int32_t);
     const size_t ws = (size_t)d.sm_count * 2 * (size_t)tiles_of_tokens(max_tokens) * 8 * kFtTileRows * sizeof(float);
     e = cudaMalloc(&p->ctl, p->ctl_bytes);
-    if (e == cudaSuccess) e = cudaMemset(p->ctl, 0, p->ctl_bytes);
+    if (e == cudaSuccess) e = clear_memory(p->ctl, p->ctl_bytes);
     if (e == cudaSuccess) e = cudaMalloc(&p->workspace, ws);
     if (e == cudaSuccess && wq_prepares(tiles_of_tokens(max_tokens)))
         e = cudaMalloc(&p->prepared, (size_t)cdiv(K, kWqChunkK) *
@@ -455,7 +463,7 @@ extern "C" int gemm_moe_plan(const gemm_moe_desc *desc, gemm_moe_plan_t *out)
                  n_h = up((size_t)p->h_rows * d.inter * (d.weights == GEMM_MOE_BF16 ? 4 : 2)),
                  n_part = up((size_t)q.sm_count * 2 * tiles_of_tokens(d.max_tokens) * 8 * kFtTileRows * 4);
     e = cudaMalloc(&p->ctl, p->ctl_bytes);
-    if (e == cudaSuccess) e = cudaMemset(p->ctl, 0, p->ctl_bytes);
+    if (e == cudaSuccess) e = clear_memory(p->ctl, p->ctl_bytes);
     if (e == cudaSuccess) e = cudaMalloc(&p->ws, n_logits + 2 * n_ids + n_h + n_part);
     if (e != cudaSuccess) {
         gemm_moe_plan_destroy(p);
