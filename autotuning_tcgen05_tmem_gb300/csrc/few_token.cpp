@@ -405,6 +405,7 @@ struct gemm_moe_plan_s {
     float *logits = nullptr, *weights = nullptr, *partials = nullptr;
     int32_t *ids = nullptr;
     void *h = nullptr;
+    float *h_powers = nullptr;
 };
 
 extern "C" void gemm_moe_plan_destroy(gemm_moe_plan_t p)
@@ -454,17 +455,21 @@ extern "C" int gemm_moe_plan(const gemm_moe_desc *desc, gemm_moe_plan_t *out)
     p->sm_count = q.sm_count;
     p->smem_limit = q.smem_per_block;
     const int64_t pairs = (int64_t)d.max_tokens * d.top_k;
+    const bool wq = d.weights == GEMM_MOE_WQ;
     p->max_tiles_up = std::min<int64_t>(d.experts, pairs) * cdiv(d.inter, 64);
     p->ctl_bytes = (size_t)(kMoeCtlHead + p->max_tiles_up + cdiv(d.hidden, kFtTileRows)) * sizeof(int32_t);
     p->h_rows = pairs + 64;   // a box of rows may reach past the last one
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     const size_t n_logits = up((size_t)kMoeMaxSlices * d.max_tokens * d.experts * 4),
                  n_ids = up((size_t)pairs * 4),
-                 n_h = up((size_t)p->h_rows * d.inter * (d.weights == GEMM_MOE_BF16 ? 4 : 2)),
+                 n_h = up(wq ? (size_t)cdiv(d.inter, kWqChunkK) * p->h_rows * kWqChunkK * 2 : (size_t)p->h_rows * d.inter * 4),
+                 n_powers = wq ? up((size_t)cdiv(d.inter, kWqChunkK) * p->h_rows * 16) : 0,
                  n_part = up((size_t)q.sm_count * 2 * tiles_of_tokens(d.max_tokens) * 8 * kFtTileRows * 4);
     e = cudaMalloc(&p->ctl, p->ctl_bytes);
     if (e == cudaSuccess) e = clear_memory(p->ctl, p->ctl_bytes);
-    if (e == cudaSuccess) e = cudaMalloc(&p->ws, n_logits + 2 * n_ids + n_h + n_part);
+    if (e == cudaSuccess) e = cudaMalloc(&p->ws, n_logits + 2 * n_ids + n_h + n_powers + n_part);
+    // h past the last feature stays what it is here: zeros.
+    if (e == cudaSuccess && wq) e = clear_memory(p->ws + n_logits + 2 * n_ids, n_h + n_powers);
     if (e != cudaSuccess) {
         gemm_moe_plan_destroy(p);
         return cuda_err(e, "cudaMalloc(moe plan)");
@@ -474,6 +479,7 @@ extern "C" int gemm_moe_plan(const gemm_moe_desc *desc, gemm_moe_plan_t *out)
     p->ids = reinterpret_cast<int32_t *>(at), at += n_ids;
     p->weights = reinterpret_cast<float *>(at), at += n_ids;
     p->h = at, at += n_h;
+    p->h_powers = reinterpret_cast<float *>(at), at += n_powers;
     p->partials = reinterpret_cast<float *>(at);
     *out = p;
     return GEMM_OK;
@@ -555,7 +561,8 @@ static int moe_run(gemm_moe_plan_t p, int64_t tokens, const void *x, const void 
     k.off_ring = kFtCtl + kTables;
     k.off_x = wq ? round_up(4u * (uint32_t)k.chunk_bytes, 1024) : (uint32_t)step_k * 256u;
     k.off_meta = k.off_x + (uint32_t)(moe_stage_rows(wq ? FT_MOE_W4 : FT_MOE_BF16, k.t8) * step_k * 2);
-    k.stage_bytes = wq ? round_up(k.off_meta + meta_bytes(k.t8), 1024) : k.off_meta;
+    k.off_powers = k.off_meta + meta_bytes(k.t8);
+    k.stage_bytes = wq ? round_up(k.off_powers + (uint32_t)k.t8 * 16u, 1024) : k.off_meta;
     static_assert(8 * (2 * kMoeMaxExperts + 2 * kMoeMaxTopK) * 4 <= kRouteWeightBytes, "a token group's choice");
     const int64_t room = p->smem_limit - 1024 - k.off_ring - red - acc;
     k.stages = (int32_t)std::min<int64_t>(kFtMaxStages, room / k.stage_bytes);
@@ -586,6 +593,7 @@ static int moe_run(gemm_moe_plan_t p, int64_t tokens, const void *x, const void 
     k.ids = p->ids;
     k.weights = p->weights;
     k.h = p->h;
+    k.h_powers = p->h_powers;
     k.h_rows = (int32_t)p->h_rows;
     k.partials = p->partials;
     k.ctl = p->ctl;
@@ -599,9 +607,8 @@ static int moe_run(gemm_moe_plan_t p, int64_t tokens, const void *x, const void 
     k.up_spans = 1;                     // 2·inter is a multiple of 64
     k.down_spans = d.hidden % 64 == 0;
     rc = wq ? encode_rows(&m.x, x, d.hidden, tokens, (int)tokens) : encode_tokens(&m.x, x, d.hidden, tokens, k.t8, step_k / 64);
-    for (int i = 0; i < 4 && !rc && (1 << i) <= nt; ++i)
-        rc = wq ? encode_rows(&m.h[i], p->h, d.inter, p->h_rows, 8 << i)
-                : encode_tokens(&m.h[i], p->h, d.inter, 2 * p->h_rows, 8 << i, step_k / 64);
+    for (int i = 0; i < 4 && !rc && !wq && (1 << i) <= nt; ++i)
+        rc = encode_tokens(&m.h[i], p->h, d.inter, 2 * p->h_rows, 8 << i, step_k / 64);
     if (!rc && !wq) {
         rc = encode_stack(&m.gate_up, gate_up, (uint64_t)d.inter * 2, (uint64_t)d.hidden, (uint64_t)d.experts,
                           (uint32_t)step_k, 2);

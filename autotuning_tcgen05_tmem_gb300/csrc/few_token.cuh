@@ -280,35 +280,58 @@ __device__ __forceinline__ void load_tokens(uint32_t dst, const CUtensorMap *m, 
 // Conversion of R rows of 256 at once (so that their latencies overlap; one warp, 16
 // bytes w[q] of each a lane): out[q] the lane's 16 bytes, scale[q] the power of two
 // (all lanes), sum[q] the sum over the lane's group in the codes' unit.
+//
+// Rows are bf16, or (powers not 0) rows of h of 4-bit experts: fp16 with a power of two
+// for each 64, the row's four at powers + 16·r[q], infinite where the 64 hold an infinity or NaN
+// (as scale is).  Brought to the row's largest power only values below 2^-20 of the
+// largest lose bits.
 template <int R>
-__device__ __forceinline__ void ft_convert(const uint32_t (&w)[R][4], int gpc, uint32_t (&out)[R][4], float (&scale)[R],
-                                           float (&sum)[R])
+__device__ __forceinline__ void ft_convert(const uint32_t (&w)[R][4], uint32_t powers, const int (&r)[R], int lane, int gpc,
+                                           uint32_t (&out)[R][4], float (&scale)[R], float (&sum)[R])
 {
-    uint32_t e[R];
+    float f[R];            // of the lane's values
+    if (powers) {
 #pragma unroll
-    for (int q = 0; q < R; ++q) {
-        auto abs2 = [](uint32_t u) { return __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&u)); };
-        const __nv_bfloat162 mx = __hmax2(__hmax2(abs2(w[q][0]), abs2(w[q][1])), __hmax2(abs2(w[q][2]), abs2(w[q][3])));
-        const uint32_t mb = *reinterpret_cast<const uint32_t *>(&mx);
-        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, max(mb & 0xFFFFu, mb >> 16)) << 16;
-        e[q] = max(top >> 23, 15u);                                   // biased exponent of the largest
+        for (int q = 0; q < R; ++q) {
+            const float4 all = ld_shared_v4(powers + (uint32_t)r[q] * 16u);
+            const float e = (lane & 16) ? (lane & 8 ? all.w : all.z) : lane & 8 ? all.y : all.x;
+            scale[q] = fmaxf(fmaxf(all.x, all.y), fmaxf(all.z, all.w));
+            const float inv = __uint_as_float(0x7F000000u - __float_as_uint(scale[q]));   // of a power of two
+            f[q] = scale[q] == INFINITY ? (e == INFINITY ? 1.0f : 0.0f) : e * inv;
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            auto abs2 = [](uint32_t u) { return __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&u)); };
+            const __nv_bfloat162 mx = __hmax2(__hmax2(abs2(w[q][0]), abs2(w[q][1])), __hmax2(abs2(w[q][2]), abs2(w[q][3])));
+            const uint32_t mb = *reinterpret_cast<const uint32_t *>(&mx);
+            const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, max(mb & 0xFFFFu, mb >> 16)) << 16;
+            const uint32_t e = max(top >> 23, 15u);                               // biased exponent of the largest
+            f[q] = __uint_as_float((268u - min(e, 254u)) << 23);                  // 2^(14 - exponent)
+            scale[q] = e == 255u ? INFINITY : __uint_as_float((e - 14u) << 23);   // 2^(exponent - 14)
+        }
     }
 #pragma unroll
     for (int q = 0; q < R; ++q) {
-        const float inv = __uint_as_float((268u - min(e[q], 254u)) << 23);   // 2^(14 - exponent)
         float xs[8];
+        if (powers) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float f = k & 1 ? inv * 0.0625f : inv;
-            xs[2 * k] = bf16_lo(w[q][k]) * f, xs[2 * k + 1] = bf16_hi(w[q][k]) * f;
+            for (int k = 0; k < 4; ++k) {
+                const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&w[q][k]));
+                xs[2 * k] = h.x, xs[2 * k + 1] = h.y;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) xs[2 * k] = bf16_lo(w[q][k]), xs[2 * k + 1] = bf16_hi(w[q][k]);
         }
-        if (e[q] == 255u) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) xs[k] *= k & 2 ? f[q] * 0.0625f : f[q];
+        if (!powers && scale[q] == INFINITY) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 xs[k] = isinf(xs[k]) ? copysignf(k & 2 ? 1024.0f : 16384.0f, xs[k]) : (isnan(xs[k]) ? xs[k] : 0.0f);
         }
         sum[q] = fmaf(xs[2] + xs[3] + (xs[6] + xs[7]), 16.0f, xs[0] + xs[1] + (xs[4] + xs[5]));
-        scale[q] = e[q] == 255u ? INFINITY : __uint_as_float((e[q] - 14u) << 23);   // 2^(exponent - 14)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const __half2 h = __floats2half2_rn(xs[2 * k], xs[2 * k + 1]);
@@ -334,8 +357,8 @@ __device__ __forceinline__ uint32_t ft_converted_place(int r, int lane)
 // Converts rows of a stage in place (one warp): row r[q] of the tile is token column
 // i[q], and only the first n count.
 template <int R>
-__device__ __forceinline__ void ft_convert_rows(uint32_t x, const int (&r)[R], const int (&i)[R], int n, float *meta, int t8,
-                                                int gpc, int lane)
+__device__ __forceinline__ void ft_convert_rows(uint32_t x, uint32_t powers, const int (&r)[R], const int (&i)[R], int n,
+                                                float *meta, int t8, int gpc, int lane)
 {
     uint32_t w[R][4], out[R][4];
     float scale[R], sum[R];
@@ -344,7 +367,7 @@ __device__ __forceinline__ void ft_convert_rows(uint32_t x, const int (&r)[R], c
         const uint4 v = lds128(x + (uint32_t)r[q] * 512u + (uint32_t)lane * 16u);
         w[q][0] = v.x, w[q][1] = v.y, w[q][2] = v.z, w[q][3] = v.w;
     }
-    ft_convert<R>(w, gpc, out, scale, sum);
+    ft_convert<R>(w, powers, r, lane, gpc, out, scale, sum);
     __syncwarp();                                                     // every lane holds its 16 bytes
 #pragma unroll
     for (int q = 0; q < R; ++q) {
@@ -360,19 +383,20 @@ __device__ __forceinline__ void ft_convert_rows(uint32_t x, const int (&r)[R], c
 // so that few tokens keep all warps busy).  A warp without a token waits and arrives
 // like the others: its arrival is what holds the slot until it has seen this lap.
 template <typename F>
-__device__ __forceinline__ void ft_convert_step(const Ring &ring, const RingPos &pos, const WaitCtl &ctl, uint32_t x, int n_tok,
-                                                int first, int warps, F row, float *meta, int t8, int gpc, int lane)
+__device__ __forceinline__ void ft_convert_step(const Ring &ring, const RingPos &pos, const WaitCtl &ctl, uint32_t x,
+                                                uint32_t powers, int n_tok, int first, int warps, F row, float *meta,
+                                                int t8, int gpc, int lane)
 {
     ring.wait_full(pos, ctl);
     int i = first;
     for (; i + warps < n_tok; i += 3 * warps) {
         const int c[3] = {i, i + warps, min(i + 2 * warps, n_tok - 1)};
         const int r[3] = {row(c[0]), row(c[1]), row(c[2])};
-        ft_convert_rows<3>(x, r, c, i + 2 * warps < n_tok ? 3 : 2, meta, t8, gpc, lane);
+        ft_convert_rows<3>(x, powers, r, c, i + 2 * warps < n_tok ? 3 : 2, meta, t8, gpc, lane);
     }
     if (i < n_tok) {
         const int c[1] = {i}, r[1] = {row(i)};
-        ft_convert_rows<1>(x, r, c, 1, meta, t8, gpc, lane);
+        ft_convert_rows<1>(x, powers, r, c, 1, meta, t8, gpc, lane);
     }
     fence_proxy_async_smem();   // the slot's next copy writes what plain stores wrote here
     __syncwarp();

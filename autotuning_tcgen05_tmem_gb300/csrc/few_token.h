@@ -162,7 +162,7 @@ struct MoeParams {
     int32_t route_reduce;              // the last slice of a token group chooses for all CTAs
     int32_t max_tiles_up;
     int32_t stages;
-    uint32_t off_route, off_ring, stage_bytes, off_x, off_meta, off_red, off_acc;
+    uint32_t off_route, off_ring, stage_bytes, off_x, off_meta, off_powers, off_red, off_acc;
     const void *x, *router;
     const uint8_t *gate_up, *down;     // 4-bit: packed experts
     const int32_t *ids_in;             // routed by the caller
@@ -175,8 +175,11 @@ struct MoeParams {
     float *logits;                     // [slices][T][E] partial router products
     int32_t *ids;                      // [T][top_k]
     float *weights;
-    void *h;                           // [T·top_k (+ padding)][I] activations, by expert; bf16
-                                       // experts: high parts, then (h_rows rows on) low parts
+    // Activations between the products, T·top_k rows (+ padding: h_rows) by expert.  bf16
+    // experts: [I] bf16, high parts, then (h_rows rows on) low parts.  4-bit experts: fp16,
+    // [256 K][row][256], with powers of two for each 64 of a row, [256 K][row][4].
+    void *h;
+    float *h_powers;
     int32_t h_rows;
     float *partials;                   // two tiles for each CTA
     int32_t *ctl;                      // [0] status, [2..3] arrivals (64-bit), [8..15] router groups,

@@ -7,7 +7,7 @@
 // Bound by the weights of the experts that were chosen, each read once however
 // many tokens chose it: 1 token, 2 of 8 bf16 experts of 4096x14336, 119 us, 5.9 TB/s (87%
 // of a copy); 64 tokens, 4 of 32 of 4096x2048, 303 us, 5.3 TB/s; 16 tokens, 8 of 64 4-bit
-// experts, 187 us, 4.0 TB/s (the multiplications and conversions of 4-bit steps, not the
+// experts, 197 us, 3.8 TB/s (the multiplications and conversions of 4-bit steps, not the
 // memory, bound that one).  Small layers are bound by the chain of phases: 1 token, 8 of
 // 64 of 2048x1024, takes 38 us for 15 us of weights.  One cooperative launch, one CTA to
 // an SM, three phases:
@@ -484,7 +484,7 @@ struct MoeKernel {
         auto step = [&](int n_tok, int off, bool up) {
             const uint32_t st = ring.stage(pos);
             float *const meta = reinterpret_cast<float *>(gbase + (st - base) + p.off_meta);
-            ft_convert_step(ring, pos, ctl, st + p.off_x, n_tok, first, kConverters,
+            ft_convert_step(ring, pos, ctl, st + p.off_x, up ? 0u : st + p.off_powers, n_tok, first, kConverters,
                             [&](int i) { return up ? (int)rt->token[off + i] : i; }, meta, p.t8, p.gpc, lane);
             first = first + 1 == kConverters ? 0 : first + 1;
             pos.next(p.stages);
@@ -562,20 +562,25 @@ struct MoeKernel {
             };
             auto begin = [&](const RingPos &r) {
                 const int nt = tiles_of(rt->down_count[w.a]);
-                mbar_arrive_expect_tx(ring.full(r), weight_bytes(false, w.t) + (uint32_t)((FMT == 0 ? 2 : 1) * kBoxes * nt * 1024));
+                mbar_arrive_expect_tx(ring.full(r), weight_bytes(false, w.t) + (uint32_t)(FMT == 0 ? 2 * kBoxes * nt * 1024 : nt * 8 * (512 + 16)));
                 weights(false, rt->down_expert[w.a], w.t, w.kb, ring.stage(r), ring.full(r));
                 next(w);
             };
             auto rows_of_h = [&](const RingPos &r) {
                 const int nt = tiles_of(rt->down_count[h.a]);
-                const CUtensorMap *hm = nt == 1 ? &m.h[0] : nt == 2 ? &m.h[1] : nt == 4 ? &m.h[2] : &m.h[3];
                 const int row = rt->down_offset[h.a];
                 if constexpr (FMT == 0) {
+                    const CUtensorMap *hm = nt == 1 ? &m.h[0] : nt == 2 ? &m.h[1] : &m.h[2];   // moe_down_tokens
                     const uint32_t box = (uint32_t)nt * 1024u;
                     for (uint32_t part = 0; part < 2; ++part)
                         load_tokens(ring.stage(r) + p.off_x + part * kBoxes * box, hm, ring.full(r), h.kb * kBoxes, kBoxes,
                                     row + (int)part * p.h_rows, box, p.h_spans);
-                } else tma_load_2d(ring.stage(r) + p.off_x, hm, ring.full(r), h.kb * kWqChunkK, row);
+                } else {
+                    const int64_t at = (int64_t)h.kb * p.h_rows + row;
+                    bulk_load(ring.stage(r) + p.off_x, static_cast<const uint8_t *>(p.h) + at * 512, (uint32_t)nt * 4096u,
+                              ring.full(r));
+                    bulk_load(ring.stage(r) + p.off_powers, p.h_powers + at * 4, (uint32_t)nt * 128u, ring.full(r));
+                }
                 next(h);
             };
             const int n = (int)(s1 - s0);
@@ -632,6 +637,51 @@ struct MoeKernel {
             }
     }
 
+    // h of tile j for n_tok tokens from row `off` on, in the form that the down phase
+    // multiplies.  bf16 experts: as a sum of two bf16 numbers, 16 significant bits; one, 8
+    // bits, would add as much error to y as the rounding of y does, and the second doubles
+    // only the products of h.  4-bit experts: in fp16, as their products read it anyway, 11
+    // bits and an eighth of that error; a power of two for each 64 features of a row takes
+    // the place of the exponents that fp16 lacks.
+    static __device__ __forceinline__ void store_h(const MoeParams &p, const float *red, int n_tok, int off, int j, int tid)
+    {
+        auto value = [&](int t, int f) {
+            const float *const at = red + t * kFtRowStride + ft_gate_row(f);
+            return ft_act(at[0], p.act) * at[8];
+        };
+        if constexpr (FMT == 0) {
+            __nv_bfloat16 *const hs = static_cast<__nv_bfloat16 *>(p.h);
+            for (int e = tid; e < 64 * n_tok; e += kFtStorers) {
+                const int f = e & 63, t = e >> 6, col = j * 64 + f;
+                if (col >= p.I) continue;
+                const float v = value(t, f);
+                const __nv_bfloat16 high = __float2bfloat16_rz(v);   // (a finite one stays finite)
+                hs[(int64_t)(off + t) * p.I + col] = high;
+                hs[(int64_t)(p.h_rows + off + t) * p.I + col] =
+                    __float2bfloat16_rn(isinf(v) ? 0.0f : v - __bfloat162float(high));
+            }
+        } else {
+            const int lane = tid & 31;
+            const bool second = j * 64 + 32 < p.I;   // I is a multiple of 32
+            for (int t = tid >> 5; t < n_tok; t += kFtStorers / 32) {
+                float v[2] = {value(t, lane), second ? value(t, lane + 32) : 0.0f};
+                const uint32_t top = __reduce_max_sync(
+                    0xFFFFFFFFu, max(__float_as_uint(v[0]) & 0x7FFFFFFFu, __float_as_uint(v[1]) & 0x7FFFFFFFu));
+                const uint32_t e = max(top >> 23, 15u);              // biased exponent of the largest
+                const float inv = __uint_as_float((268u - min(e, 254u)) << 23);
+                const int64_t row = (int64_t)(j >> 2) * p.h_rows + off + t;
+                __half *const out = static_cast<__half *>(p.h) + row * kWqChunkK + (j & 3) * 64 + lane;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    if (e == 255u) v[q] = isinf(v[q]) ? copysignf(16384.0f, v[q]) : isnan(v[q]) ? v[q] : 0.0f;
+                    else v[q] *= inv;
+                    if (q == 0 || second) out[q * 32] = __float2half_rn(v[q]);
+                }
+                if (lane == 0) p.h_powers[row * 4 + (j & 3)] = e == 255u ? INFINITY : __uint_as_float((e - 14u) << 23);
+            }
+        }
+    }
+
     // The storers: h of the up phase's tiles, the meeting of all CTAs, y.
     static __device__ __forceinline__ void finish(const MoeParams &p, const HandOver &hand, const WaitCtl &ctl,
                                                   const RouteTables *rt, float *yacc, volatile int32_t *flags, int tid)
@@ -656,25 +706,7 @@ struct MoeKernel {
                 last = ft_exchange(p.partials, p.t8, red, n_tok, run.k == 0, p.ctl + kMoeCtlHead + tile, first, pieces, flags + 1,
                                    tid);
             }
-            // The down product reads h in bf16.  bf16 experts: as a sum of two parts, 16
-            // significant bits together.  One part, 8 bits, would add as much error to
-            // y as its own rounding does; the second doubles only the products of h.
-            __nv_bfloat16 *const hs = static_cast<__nv_bfloat16 *>(p.h);
-            if (last)
-                for (int e = tid; e < 64 * n_tok; e += kFtStorers) {
-                    const int f = e & 63, t = e >> 6, col = j * 64 + f;
-                    if (col >= p.I) continue;
-                    const float *const at = red + t * kFtRowStride + ft_gate_row(f);
-                    const float v = ft_act(at[0], p.act) * at[8];
-                    if constexpr (FMT == 0) {
-                        const __nv_bfloat16 high = __float2bfloat16_rz(v);   // (a finite one stays finite)
-                        hs[(int64_t)(off + t) * p.I + col] = high;
-                        hs[(int64_t)(p.h_rows + off + t) * p.I + col] =
-                            __float2bfloat16_rn(isinf(v) ? 0.0f : v - __bfloat162float(high));
-                    } else {
-                        hs[(int64_t)(off + t) * p.I + col] = __float2bfloat16_rn(v);
-                    }
-                }
+            if (last) store_h(p, red, n_tok, off, j, tid);
             ft_give_back(hand, h, lane);
         }
         fence_proxy_async_all();
@@ -761,8 +793,8 @@ __global__ void __launch_bounds__(ft_threads(FMT, NTMAX), 1)
     }
     if (threadIdx.x == 32 * K::kCopier) {
         prefetch_tmap(&m.x);
-        prefetch_tmap(&m.h[0]);
         if (FMT == 0) {
+            prefetch_tmap(&m.h[0]);
             prefetch_tmap(&m.gate_up);
             prefetch_tmap(&m.down);
         }

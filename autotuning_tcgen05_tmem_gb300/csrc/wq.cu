@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(ft_threads(FT_PRODUCT, NT), 1)
         RingPos pos;
         for (int i = 0; i < n_steps; ++i, pos.next(p.stages)) {
             float *const meta = reinterpret_cast<float *>(gbase + (ring.stage(pos) - base) + p.off_meta);
-            ft_convert_step(ring, pos, ctl, ring.stage(pos) + p.off_x, p.T, (warp + i) % max(converters, 1), converters,
+            ft_convert_step(ring, pos, ctl, ring.stage(pos) + p.off_x, 0u, p.T, (warp + i) % max(converters, 1), converters,
                             [](int r) { return r; }, meta, p.t8, p.gpc, lane);
         }
     } else if (warp >= kFirstStorer) {
@@ -274,7 +274,8 @@ __global__ void __launch_bounds__(256) wq_prepare_kernel(const __grid_constant__
     const uint32_t w[1][4] = {{v.x, v.y, v.z, v.w}};
     uint32_t out[1][4];
     float scale[1], sum[1];
-    ft_convert<1>(w, p.gpc, out, scale, sum);
+    const int row[1] = {0};
+    ft_convert<1>(w, 0u, row, lane, p.gpc, out, scale, sum);
     uint8_t *const piece = p.out + (int64_t)kb * p.piece_bytes;
     float *const meta = reinterpret_cast<float *>(piece + p.T * 512);
     *reinterpret_cast<uint4 *>(piece + t * 512 + ft_converted_place(t, lane)) = make_uint4(out[0][0], out[0][1], out[0][2], out[0][3]);

@@ -672,7 +672,7 @@ void gemm_wq_plan_destroy(gemm_wq_plan_t plan);
  *   (the lowest index among equals; NaN above all), w_j = p_j, or p_j / Σ p_j
  *   over the chosen when `normalize`;
  *   h_e = act(x · Gate_e) ⊙ (x · Up_e), held in 16 significant bits with bf16
- *         experts, rounded to bf16 with packed ones;
+ *         experts and in 11 (fp16 with a power of two for each 64 features) with packed ones;
  *   y = Σ_j w_j · (h_{e_j} · Down_{e_j}) (+ R).
  * router is bf16 [hidden, experts]; gate_up [experts, hidden, 2·inter] with 32
  * gate and 32 up columns in turn; down [experts, inter, hidden]: bf16, or
