@@ -353,6 +353,8 @@ extern "C" int gemm_wq_run(gemm_wq_plan_t p, int64_t tokens, const void *x, cons
     const int smem = (int)(k.off_red + red + 1024);
 
     k.packed = static_cast<const uint8_t *>(packed);
+    k.x = x;
+    k.K = (int32_t)p->K;
     k.bias = p->epi != GEMM_EPI_NONE ? bias : nullptr;
     k.residual = R;
     k.y = y;

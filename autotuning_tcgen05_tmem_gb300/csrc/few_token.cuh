@@ -274,16 +274,16 @@ __device__ __forceinline__ void load_tokens(uint32_t dst, const CUtensorMap *m, 
 // Activations in a stage: one row of 512 bytes for each token, 256 bf16 as they
 // come, converted in place: the 16 bytes at (j ^ (row % 8))·64 + t·16 are
 // k = 32j + 8t .. + 7.  Beside them (off_meta) for each token its power of two and,
-// for each group, its sum.  An infinity stays one (power of two inf, the infinite
-// values ±2^14 and the others 0), a NaN too.
+// for each group, its sum.  Where a row of 256 holds an infinity the power of two is NaN,
+// which makes the token's sums NaN; ft_resolve finds what they are.
 
 // Conversion of R rows of 256 at once (so that their latencies overlap; one warp, 16
 // bytes w[q] of each a lane): out[q] the lane's 16 bytes, scale[q] the power of two
 // (all lanes), sum[q] the sum over the lane's group in the codes' unit.
 //
 // Rows are bf16, or (powers not 0) rows of h of 4-bit experts: fp16 with a power of two
-// for each 64, the row's four at powers + 16·r[q], infinite where the 64 hold an infinity or NaN
-// (as scale is).  Brought to the row's largest power only values below 2^-20 of the
+// for each 64, the row's four at powers + 16·r[q], infinite where the 64 hold an infinity or
+// NaN.  Brought to the row's largest power only values below 2^-20 of the
 // largest lose bits.
 template <int R>
 __device__ __forceinline__ void ft_convert(const uint32_t (&w)[R][4], uint32_t powers, const int (&r)[R], int lane, int gpc,
@@ -296,8 +296,8 @@ __device__ __forceinline__ void ft_convert(const uint32_t (&w)[R][4], uint32_t p
             const float4 all = ld_shared_v4(powers + (uint32_t)r[q] * 16u);
             const float e = (lane & 16) ? (lane & 8 ? all.w : all.z) : lane & 8 ? all.y : all.x;
             scale[q] = fmaxf(fmaxf(all.x, all.y), fmaxf(all.z, all.w));
-            const float inv = __uint_as_float(0x7F000000u - __float_as_uint(scale[q]));   // of a power of two
-            f[q] = scale[q] == INFINITY ? (e == INFINITY ? 1.0f : 0.0f) : e * inv;
+            f[q] = e * __uint_as_float(0x7F000000u - __float_as_uint(scale[q]));   // 1 over a power of two
+            if (scale[q] == INFINITY) scale[q] = NAN;
         }
     } else {
 #pragma unroll
@@ -308,7 +308,7 @@ __device__ __forceinline__ void ft_convert(const uint32_t (&w)[R][4], uint32_t p
             const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, max(mb & 0xFFFFu, mb >> 16)) << 16;
             const uint32_t e = max(top >> 23, 15u);                               // biased exponent of the largest
             f[q] = __uint_as_float((268u - min(e, 254u)) << 23);                  // 2^(14 - exponent)
-            scale[q] = e == 255u ? INFINITY : __uint_as_float((e - 14u) << 23);   // 2^(exponent - 14)
+            scale[q] = e == 255u ? NAN : __uint_as_float((e - 14u) << 23);   // 2^(exponent - 14)
         }
     }
 #pragma unroll
@@ -326,11 +326,6 @@ __device__ __forceinline__ void ft_convert(const uint32_t (&w)[R][4], uint32_t p
         }
 #pragma unroll
         for (int k = 0; k < 8; ++k) xs[k] *= k & 2 ? f[q] * 0.0625f : f[q];
-        if (!powers && scale[q] == INFINITY) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                xs[k] = isinf(xs[k]) ? copysignf(k & 2 ? 1024.0f : 16384.0f, xs[k]) : (isnan(xs[k]) ? xs[k] : 0.0f);
-        }
         sum[q] = fmaf(xs[2] + xs[3] + (xs[6] + xs[7]), 16.0f, xs[0] + xs[1] + (xs[4] + xs[5]));
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -516,6 +511,50 @@ __device__ __forceinline__ void ft_scale_w4(Acc<NW> &acc)
         for (int n = 0; n < NW; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc.v[m][n][i] *= 16777216.0f;
+}
+
+// A sum that is not finite, as the definition gives it.  Where the activations hold
+// infinities or NaN it is the sum of (code - zero) · scale · x over those alone, product by
+// product: an infinity, or NaN (of opposite ones, of a code that is its zero point).
+// Otherwise it stands as it is (v).  Read again from global memory, by the storers where they
+// meet such a sum: a look at each step's powers cost the products 3%.  (A lean function of
+// its own: one with more registers, called or not, cost the kernels 4 to 10%.)
+//
+// chunk: of the column group, K block 0; step: bytes from one K block to the next; where:
+// row (of 32) + 32·gpc + 512·has_zeros.
+__device__ __forceinline__ float ft_weight(const uint8_t *c, uint32_t where, int k)
+{
+    const int i = k & 7, row = where & 31, gpc = where >> 5 & 15, j = k >> 5 & 7;
+    const int at = (j * gpc >> 3) * 32 + (row & 7) * 4 + (row >> 3);
+    const int byte = j * 512 + ((row & 7) * 4 + (k >> 3 & 3)) * 16 + (row >> 3) * 4 + ((i >> 1) + 4 * (i & 1)) / 2;
+    const int zero = where >> 9 ? c[kWqChunkCodes + gpc * 64 + at] : 8;
+    return (float)((c[byte] >> (i & 2 ? 4 : 0) & 15) - zero) *
+           __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(c + kWqChunkCodes)[at]);
+}
+
+// x: the token's row of K bf16.
+__device__ __noinline__ float ft_resolve(const uint8_t *chunk, uint32_t step, uint32_t where, const __nv_bfloat16 *x, int K,
+                                         float v)
+{
+    float sum = 0.0f;
+    bool found = false;
+#pragma unroll 1
+    for (int k = 0; k < K; ++k) {
+        if ((k & 7) == 0) {   // eight at once: none?
+            const uint4 u = *reinterpret_cast<const uint4 *>(x + k);
+            auto any = [](uint32_t w) { return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u; };
+            if (!any(u.x) && !any(u.y) && !any(u.z) && !any(u.w)) {
+                k += 7;
+                continue;
+            }
+        }
+        const uint32_t e = __bfloat16_as_ushort(x[k]);
+        if ((e & 0x7FFFu) < 0x7F80u) continue;
+        sum += ft_weight(chunk + (int64_t)(k >> 8) * step, where, k) * __uint_as_float(e << 16);
+        found = true;
+        if (sum != sum) break;
+    }
+    return found ? sum : v;
 }
 
 // --- bf16 weights ----------------------------------------------------------------

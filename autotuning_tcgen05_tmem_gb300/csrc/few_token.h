@@ -130,6 +130,8 @@ struct WqParams {
     const uint8_t *packed;
     const uint8_t *prepared;           // converted activations, a piece for each 256 K
     uint32_t prepared_bytes;           // of a piece: T rows of 512 bytes, and the meta data
+    const void *x;
+    int32_t K;
     const void *bias, *residual;
     void *y;
     float *workspace;                  // partial tiles, two for each CTA

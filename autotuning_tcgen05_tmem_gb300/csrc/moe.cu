@@ -407,6 +407,67 @@ struct Runs {
     }
 };
 
+// Where a row of a tile of expert `expert` lies in its packed weight (ft_resolve).
+__device__ __forceinline__ const uint8_t *moe_chunk(const MoeParams &p, bool up, int expert, int tile, int row, uint32_t &step,
+                                                    uint32_t &where)
+{
+    const int ncg = up ? p.ncg_up : p.ncg_down, nkb = up ? p.nkb_up : p.nkb_down;
+    step = (uint32_t)(min(4, ncg - 4 * tile) * p.chunk_bytes);
+    where = (uint32_t)(row & 31) | (uint32_t)p.gpc << 5 | (uint32_t)p.has_zeros << 9;
+    return (up ? p.gate_up : p.down) +
+           ((int64_t)expert * ncg * nkb + wq_chunk_index(ncg, nkb, tile, 0) + (row >> 5)) * p.chunk_bytes;
+}
+
+// ft_resolve for a row of an up tile and a token.
+__device__ __forceinline__ float moe_resolve_up(const MoeParams &p, int expert, int tile, int row, int token, float v)
+{
+    uint32_t step, where;
+    const uint8_t *const chunk = moe_chunk(p, true, expert, tile, row, step, where);
+    return ft_resolve(chunk, step, where, static_cast<const __nv_bfloat16 *>(p.x) + (int64_t)token * p.H, p.H, v);
+}
+
+// The same on a row of h, in blocks of 256 features `rows` rows apart: 0 if it holds neither an
+// infinity (which lies there as ±2^14 among zeros, under an infinite power) nor NaN.
+__device__ __noinline__ float ft_resolve_h(const uint8_t *chunk, uint32_t step, uint32_t where, const __half *h,
+                                           const float *powers, int rows, int I)
+{
+    float sum = 0.0f;
+#pragma unroll 1
+    for (int k = 0; k < I; ++k) {
+        if (__ldcg(powers + ((int64_t)(k >> 8) * rows * 4 + (k >> 6 & 3))) != INFINITY) {
+            k |= 63;
+            continue;
+        }
+        const float mark = __half2float(__ldcg(h + ((int64_t)(k >> 8) * rows * kWqChunkK + (k & 255))));
+        if (mark == 0.0f) continue;
+        sum += ft_weight(chunk + (int64_t)(k >> 8) * step, where, k) * (mark != mark ? mark : mark * INFINITY);
+        if (sum != sum) break;
+    }
+    return sum;
+}
+
+// A sum over a token's experts: each resolved and weighted; those whose h is finite add
+// nothing to what the others make of it.
+__device__ __forceinline__ float moe_resolve_down(const MoeParams &p, const RouteTables *rt, int tile, int row, int token, float v)
+{
+    // All CTAs met before the down phase; this read of the count makes their h visible here.
+    ld_acquire_gpu_u64(reinterpret_cast<const uint64_t *>(p.ctl + 2));
+    float sum = 0.0f;
+    bool found = false;
+#pragma unroll 1
+    for (int a = 0; a < rt->n_down; ++a)
+#pragma unroll 1
+        for (int at = rt->down_offset[a]; at < rt->down_offset[a] + rt->down_count[a]; ++at) {
+            if (rt->token[at] != token) continue;
+            uint32_t step, where;
+            const uint8_t *const chunk = moe_chunk(p, false, rt->down_expert[a], tile, row, step, where);
+            const float one = ft_resolve_h(chunk, step, where, static_cast<const __half *>(p.h) + (int64_t)at * kWqChunkK,
+                                           p.h_powers + (int64_t)at * 4, p.h_rows, p.I);
+            if (one != 0.0f) sum += rt->weight[at] * one, found = true;   // an infinity or NaN
+        }
+    return found ? sum : v;
+}
+
 // FMT 0: bf16 experts; 1: packed 4-bit experts.  NTMAX: 8-token tiles of the call.
 template <int FMT, int NTMAX>
 struct MoeKernel {
@@ -637,13 +698,70 @@ struct MoeKernel {
             }
     }
 
+    // Two features of a row of h of 4-bit experts (a warp; v: 0 past the last), as fp16 with
+    // their 64's power of two; false where it holds an infinity or NaN, unless MARK: then the
+    // power is infinite, infinities are marked and what is finite is 0.
+    template <bool MARK>
+    static __device__ __forceinline__ bool store_row(const MoeParams &p, float (&v)[2], int at, int j, bool second, int lane)
+    {
+        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu,
+                                               max(__float_as_uint(v[0]) & 0x7FFFFFFFu, __float_as_uint(v[1]) & 0x7FFFFFFFu));
+        const uint32_t e = max(top >> 23, 15u);              // biased exponent of the largest
+        if (!MARK && e == 255u) return false;
+        const float inv = __uint_as_float((268u - min(e, 254u)) << 23);
+        const int64_t row = (int64_t)(j >> 2) * p.h_rows + at;
+        __half *const out = static_cast<__half *>(p.h) + row * kWqChunkK + (j & 3) * 64 + lane;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            if (MARK && e == 255u) v[q] = isinf(v[q]) ? copysignf(16384.0f, v[q]) : isnan(v[q]) ? v[q] : 0.0f;
+            else v[q] *= inv;
+            if (q == 0 || second) out[q * 32] = __float2half_rn(v[q]);
+        }
+        if (lane == 0) p.h_powers[row * 4 + (j & 3)] = e == 255u ? INFINITY : __uint_as_float((e - 14u) << 23);
+        return true;
+    }
+
+    // A row of h with sums that are not finite.
+    static __device__ __forceinline__ void store_row_resolved(const MoeParams &p, const float *red, const RouteTables *rt, int at,
+                                                           int j, int expert, bool second, int lane)
+    {
+        float v[2] = {0.0f, 0.0f};
+#pragma unroll 1
+        for (int q = 0; q < (second ? 2 : 1); ++q) {
+            const int row = ft_gate_row(lane + q * 32);
+            float gate = red[row], up = red[row + 8];
+            if (!(fabsf(gate) < INFINITY)) gate = moe_resolve_up(p, expert, j, row, rt->token[at], gate);
+            if (!(fabsf(up) < INFINITY)) up = moe_resolve_up(p, expert, j, row + 8, rt->token[at], up);
+            v[q] = ft_act(gate, p.act) * up;
+        }
+        __syncwarp();
+        store_row<true>(p, v, at, j, second, lane);
+    }
+
+    // Columns of y whose sums are not finite (one storer's).
+    static __device__ __forceinline__ void store_y_resolved(const MoeParams &p, const RouteTables *rt, const float *yacc, int tile,
+                                                         int tid)
+    {
+        const __nv_bfloat16 *const res = static_cast<const __nv_bfloat16 *>(p.residual);
+#pragma unroll 1
+        for (int e = tid; e < kFtTileRows * p.T; e += kFtStorers) {
+            const int row = e % kFtTileRows, t = e / kFtTileRows, n = tile * kFtTileRows + row;
+            float v = yacc[t * kFtRowStride + row];
+            if (n >= p.H || fabsf(v) < INFINITY) continue;
+            if (FMT == 1) v = moe_resolve_down(p, rt, tile, row, t, v);
+            const int64_t at = (int64_t)t * p.H + n;
+            static_cast<__nv_bfloat16 *>(p.y)[at] = __float2bfloat16_rn(res ? v + __bfloat162float(res[at]) : v);
+        }
+    }
+
     // h of tile j for n_tok tokens from row `off` on, in the form that the down phase
     // multiplies.  bf16 experts: as a sum of two bf16 numbers, 16 significant bits; one, 8
     // bits, would add as much error to y as the rounding of y does, and the second doubles
     // only the products of h.  4-bit experts: in fp16, as their products read it anyway, 11
     // bits and an eighth of that error; a power of two for each 64 features of a row takes
     // the place of the exponents that fp16 lacks.
-    static __device__ __forceinline__ void store_h(const MoeParams &p, const float *red, int n_tok, int off, int j, int tid)
+    static __device__ __forceinline__ void store_h(const MoeParams &p, const float *red, int n_tok, int off, int j, int expert,
+                                                   const RouteTables *rt, int tid)
     {
         auto value = [&](int t, int f) {
             const float *const at = red + t * kFtRowStride + ft_gate_row(f);
@@ -665,19 +783,8 @@ struct MoeKernel {
             const bool second = j * 64 + 32 < p.I;   // I is a multiple of 32
             for (int t = tid >> 5; t < n_tok; t += kFtStorers / 32) {
                 float v[2] = {value(t, lane), second ? value(t, lane + 32) : 0.0f};
-                const uint32_t top = __reduce_max_sync(
-                    0xFFFFFFFFu, max(__float_as_uint(v[0]) & 0x7FFFFFFFu, __float_as_uint(v[1]) & 0x7FFFFFFFu));
-                const uint32_t e = max(top >> 23, 15u);              // biased exponent of the largest
-                const float inv = __uint_as_float((268u - min(e, 254u)) << 23);
-                const int64_t row = (int64_t)(j >> 2) * p.h_rows + off + t;
-                __half *const out = static_cast<__half *>(p.h) + row * kWqChunkK + (j & 3) * 64 + lane;
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    if (e == 255u) v[q] = isinf(v[q]) ? copysignf(16384.0f, v[q]) : isnan(v[q]) ? v[q] : 0.0f;
-                    else v[q] *= inv;
-                    if (q == 0 || second) out[q * 32] = __float2half_rn(v[q]);
-                }
-                if (lane == 0) p.h_powers[row * 4 + (j & 3)] = e == 255u ? INFINITY : __uint_as_float((e - 14u) << 23);
+                if (!store_row<false>(p, v, off + t, j, second, lane))
+                    store_row_resolved(p, red + t * kFtRowStride, rt, off + t, j, expert, second, lane);
             }
         }
     }
@@ -706,7 +813,7 @@ struct MoeKernel {
                 last = ft_exchange(p.partials, p.t8, red, n_tok, run.k == 0, p.ctl + kMoeCtlHead + tile, first, pieces, flags + 1,
                                    tid);
             }
-            if (last) store_h(p, red, n_tok, off, j, tid);
+            if (last) store_h(p, red, n_tok, off, j, rt->act_expert[run.a], rt, tid);
             ft_give_back(hand, h, lane);
         }
         fence_proxy_async_all();
@@ -747,6 +854,7 @@ struct MoeKernel {
             }
             if (last) {
                 const int n0 = tile * kFtTileRows;
+                bool left = false;
                 ft_batched<8>(
                     kFtTileRows * p.T, tid, kFtStorers,
                     [&](int e) {
@@ -757,8 +865,13 @@ struct MoeKernel {
                         const int row = e % kFtTileRows, t = e / kFtTileRows, n = n0 + row;
                         if (n >= p.H) return;
                         const float v = yacc[t * kFtRowStride + row];
+                        if (FMT == 1 && !(fabsf(v) < INFINITY)) {
+                            left = true;
+                            return;
+                        }
                         y[(int64_t)t * p.H + n] = __float2bfloat16_rn(res ? v + r : v);
                     });
+                if (left) store_y_resolved(p, rt, yacc, tile, tid);
             }
             ft_storers_sync();
         }

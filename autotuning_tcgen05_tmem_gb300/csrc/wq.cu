@@ -45,10 +45,24 @@ __device__ __forceinline__ int wq_strip_row(int e, int strips, int rank, int ste
     return (rank + (e >> 4) % strips * step) * 16 + (e & 15);
 }
 
-// Epilogue of the 16-row strips rank, rank + step, ... of a tile, from red[token][row],
-// by `workers` threads.  A gated strip holds eight gates and their eight ups.
-__device__ __forceinline__ void wq_store(const WqParams &p, const float *red, int tile, int rank, int step, int tid, int workers)
+// ft_resolve for a row of a tile and a token.
+__device__ __forceinline__ float wq_resolve(const WqParams &p, int tile, int row, int t, float v)
 {
+    const int here = min(4, p.ncg - 4 * tile);
+    if (row >> 5 >= here) return v;
+    return ft_resolve(p.packed + (wq_chunk_index(p.ncg, p.nkb, tile, 0) + (row >> 5)) * p.chunk_bytes,
+                      (uint32_t)(here * p.chunk_bytes), (uint32_t)(row & 31) | (uint32_t)p.gpc << 5 | (uint32_t)p.has_zeros << 9,
+                      static_cast<const __nv_bfloat16 *>(p.x) + (int64_t)t * p.K, p.K, v);
+}
+
+// Epilogue of the 16-row strips rank, rank + step, ... of a tile, from red[token][row],
+// by `workers` threads.  A gated strip holds eight gates and their eight ups.  The sums
+// that are finite; true if the thread left others, which RESOLVE then stores.
+template <bool RESOLVE>
+__device__ __forceinline__ bool wq_store_sums(const WqParams &p, const float *red, int tile, int rank, int step, int tid,
+                                              int workers)
+{
+    bool left = false;
     constexpr int rstride = kFtRowStride;
     const __nv_bfloat16 *const bias = static_cast<const __nv_bfloat16 *>(p.bias);
     const __nv_bfloat16 *const res = static_cast<const __nv_bfloat16 *>(p.residual);
@@ -56,7 +70,7 @@ __device__ __forceinline__ void wq_store(const WqParams &p, const float *red, in
     const int strips = (8 - rank + step - 1) / step;
     if (!p.gated) {
         const int n0 = tile * kFtTileRows;
-        ft_batched<4>(
+        ft_batched<RESOLVE ? 1 : 4>(
             strips * 16 * p.T, tid, workers,
             [&](int e) {
                 const int n = n0 + wq_strip_row(e, strips, rank, step);
@@ -67,6 +81,11 @@ __device__ __forceinline__ void wq_store(const WqParams &p, const float *red, in
                 const int row = wq_strip_row(e, strips, rank, step), t = (e >> 4) / strips, n = n0 + row;
                 if (n >= p.N) return;
                 float v = red[t * rstride + row];
+                if ((fabsf(v) < INFINITY) == RESOLVE) {
+                    left = true;
+                    return;
+                }
+                if (RESOLVE) v = wq_resolve(p, tile, row, t, v);
                 if (bias) v += r.x;
                 v = ft_act(v, p.act);
                 y[(int64_t)t * p.N + n] = __float2bfloat16_rn(res ? v + r.y : v);
@@ -79,6 +98,14 @@ __device__ __forceinline__ void wq_store(const WqParams &p, const float *red, in
             const int gate_col = 64 * (o >> 5) + (o & 31);
             const float *const at = red + t * rstride + strip * 16 + (e & 7);
             float gate = at[0], up = at[8];
+            if ((fabsf(gate) < INFINITY && fabsf(up) < INFINITY) == RESOLVE) {
+                left = true;
+                continue;
+            }
+            if (RESOLVE) {
+                gate = fabsf(gate) < INFINITY ? gate : wq_resolve(p, tile, strip * 16 + (e & 7), t, gate);
+                up = fabsf(up) < INFINITY ? up : wq_resolve(p, tile, strip * 16 + (e & 7) + 8, t, up);
+            }
             if (bias) {
                 gate += __bfloat162float(bias[gate_col]);
                 up += __bfloat162float(bias[gate_col + 32]);
@@ -86,6 +113,12 @@ __device__ __forceinline__ void wq_store(const WqParams &p, const float *red, in
             y[(int64_t)t * (p.N / 2) + o] = __float2bfloat16_rn(ft_act(gate, p.act) * up);
         }
     }
+    return left;
+}
+
+__device__ __forceinline__ void wq_store(const WqParams &p, const float *red, int tile, int rank, int step, int tid, int workers)
+{
+    if (wq_store_sums<false>(p, red, tile, rank, step, tid, workers)) wq_store_sums<true>(p, red, tile, rank, step, tid, workers);
 }
 
 // The pieces of a tile are one cluster: each CTA adds up and stores the 16-row strips of

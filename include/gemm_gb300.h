@@ -613,7 +613,9 @@ int gemm_run_noalloc(int64_t M, int64_t N, int64_t K, gemm_epilogue epi, const g
  * are stated here.  Shared conventions: activations bf16 [tokens, K], weights
  * [K, N] row-major (experts [E, K, N]), outputs bf16; sums, scales and softmax
  * in fp32, one rounding of the result; 16-byte aligned device pointers; a plan
- * owns a workspace and must not run on two streams at once; runs are
+ * owns a workspace and must not run on two streams at once; an infinity or NaN
+ * reaches the outputs of its own token alone, where it gives what the formulas
+ * give (0 · inf and inf - inf are NaN); runs are
  * asynchronous on `stream`, allocate nothing and may be captured in a graph;
  * *_plan_status as gemm_plan_status; GEMM_CHECK and gemm_debug_set(4, 1) as
  * for gemm_run.
