@@ -10,11 +10,12 @@
 // the warps that multiply, and every CTA takes an equal share of the whole
 // reduction whatever the shape.
 //
-// Why not the fifth-generation tensor core: it needs 128 rows and a tensor-memory
-// operand a step, and one thread takes 44 cycles to issue a multiplication of 16 K that
-// it does in 15 (16 columns) to 32 (64).  Codes expanded into tensor memory, tokens as
+// Why not the fifth-generation tensor core: codes expanded into tensor memory, tokens as
 // its shared-memory operand and sums scaled on their way out came to 41 us for 16 tokens
-// 4096x28672 and 57 us for 64 tokens 14336x4096, where this form takes 25 and 41.
+// 4096x28672 and 57 us for 64 tokens 14336x4096, where this form takes 26 and 41.
+// Issuing the multiplications (5 us of the 57) did not bound it; expanding the codes did,
+// and the 33 KB of tokens copied with each step's 17 KB of weights.  Tokens that stay in
+// shared memory over several tiles ask for another kernel.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -266,7 +267,7 @@ __device__ __forceinline__ void load_tokens(uint32_t dst, const CUtensorMap *m, 
 //   * a bf16 activation has eight significant bits and fits fp16's eleven once a
 //     power of two brings the largest of its 256 of K into [2^14, 2^15).  Those that
 //     meet the codes four bits up are a sixteenth of it.  Only values below 2^-25
-//     of the largest lose bits, and at most 2^-36 of it.
+//     of the largest lose bits, and at most 2^-35 of it.
 // Σ (q - z)·x over a group is then Σ q·x from the tensor core (fp32 sums) minus
 // z·Σ x; the group's scale and the activations' power of two multiply it in fp32.
 // No weight is ever rounded.

@@ -6,8 +6,8 @@
 //
 // Bound by the weights of the experts that were chosen, each read once however
 // many tokens chose it: 1 token, 2 of 8 bf16 experts of 4096x14336, 119 us, 5.9 TB/s (87%
-// of a copy); 64 tokens, 4 of 32 of 4096x2048, 303 us, 5.3 TB/s; 16 tokens, 8 of 64 4-bit
-// experts, 197 us, 3.8 TB/s (the multiplications and conversions of 4-bit steps, not the
+// of a copy); 64 tokens, 4 of 32 of 4096x2048, 298 us, 5.4 TB/s; 16 tokens, 8 of 64 4-bit
+// experts, 198 us, 3.8 TB/s (the multiplications and conversions of 4-bit steps, not the
 // memory, bound that one).  Small layers are bound by the chain of phases: 1 token, 8 of
 // 64 of 2048x1024, takes 38 us for 15 us of weights.  One cooperative launch, one CTA to
 // an SM, three phases:

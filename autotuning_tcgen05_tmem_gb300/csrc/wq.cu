@@ -4,15 +4,16 @@
 // weight and lay codes, scales and zero points out for the product.
 //
 // Product: bound by the weight's bytes (K·N/2, plus scales), read once: 1 token
-// 8192x28672 with zero points 25.5 us, 4.8 TB/s (71% of a copy; 5 us of it are start-up
+// 8192x28672 with zero points 25.6 us, 4.8 TB/s (71% of a copy; 5 us of it are start-up
 // and the last exchange, then a step of 17 KB takes 0.43 us an SM where the memory alone
 // takes 0.37).  With more tokens the workers bound it: 64 tokens 14336x4096 41 us, 3,600
 // cycles a step (tensor pipe 45% busy, 1.7 instructions a cycle from two warps a
-// scheduler; four foursomes spill: 49 us).  One CTA to an SM; a copying warp
+// scheduler; four foursomes spill: 49 us), and above 32 tokens the library's bf16 GEMM
+// takes less time with four times the bytes (25 us there).  One CTA to an SM; a copying warp
 // fills a ring with a tile's packed chunks (one bulk copy for 128 columns x 256 K) and the
 // matching piece of x; up to 8 tokens a few warps convert it in place, above a kernel
-// ahead has prepared it (16 tokens 4096x28672: 25 us, 39 with converting warps; 1 token
-// 8192x28672: 26.1 and 25.4); foursomes of workers multiply, and four storers finish tiles behind them.  Tiles are cut
+// ahead has prepared it (16 tokens 4096x28672: 26 us, 39 with converting warps; 1 token
+// 8192x28672: 26.1 and 25.6); foursomes of workers multiply, and four storers finish tiles behind them.  Tiles are cut
 // along K into as many pieces as keep the SMs evenly busy (FtShare).  Where there
 // are few tiles the pieces of each are one thread-block cluster and add up through
 // distributed shared memory; else through a workspace, the CTA that arrives last

@@ -652,7 +652,9 @@ typedef struct gemm_wq_plan_s *gemm_wq_plan_t;
 /* Plan of y[t, n] = epi(Σ_k x[t, k] · W[k, n] + bias[n]) (+ R[t, n]) for up to
  * max_tokens (1..64) tokens and every epilogue of gemm_epilogue; gated ones
  * take a weight packed with `gated` and write y [tokens, N/2].  K is a multiple
- * of 8 (x's rows), at least 1; N is any (of 64 when gated). */
+ * of 8 (x's rows), at least 1; N is any (of 64 when gated).  It pays up to about
+ * 16 tokens: at 32 the bf16 GEMM of the same shape takes as long, above it takes
+ * less (64 tokens, 8192x28672: 71 us against 119). */
 int gemm_wq_plan(int64_t K, int64_t N, int32_t group, int32_t has_zeros, gemm_epilogue epi, int32_t max_tokens,
                  gemm_wq_plan_t *out);
 
