@@ -523,39 +523,41 @@ __device__ __forceinline__ void ft_scale_w4(Acc<NW> &acc)
 //
 // chunk: of the column group, K block 0; step: bytes from one K block to the next; where:
 // row (of 32) + 32·gpc + 512·has_zeros.
-__device__ __forceinline__ float ft_weight(const uint8_t *c, uint32_t where, int k)
+//
+// Adds what eight activations from k on (16-bit, of a size from `least` on: infinities, and
+// NaN above `nan`) make of their weights.
+__device__ __forceinline__ void ft_add_special(const uint8_t *chunk, uint32_t step, uint32_t where, int k, const uint4 &u,
+                                               uint32_t least, uint32_t nan, float &sum)
 {
-    const int i = k & 7, row = where & 31, gpc = where >> 5 & 15, j = k >> 5 & 7;
+    const uint8_t *const c = chunk + (int64_t)(k >> 8) * step;
+    const int row = where & 31, gpc = where >> 5 & 15, j = k >> 5 & 7;
     const int at = (j * gpc >> 3) * 32 + (row & 7) * 4 + (row >> 3);
-    const int byte = j * 512 + ((row & 7) * 4 + (k >> 3 & 3)) * 16 + (row >> 3) * 4 + ((i >> 1) + 4 * (i & 1)) / 2;
+    const uint32_t word = *reinterpret_cast<const uint32_t *>(c + j * 512 + ((row & 7) * 4 + (k >> 3 & 3)) * 16 + (row >> 3) * 4);
+    const float scale = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(c + kWqChunkCodes)[at]);
     const int zero = where >> 9 ? c[kWqChunkCodes + gpc * 64 + at] : 8;
-    return (float)((c[byte] >> (i & 2 ? 4 : 0) & 15) - zero) *
-           __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(c + kWqChunkCodes)[at]);
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t e = (i < 4 ? (i < 2 ? u.x : u.y) : (i < 6 ? u.z : u.w)) >> (16 * (i & 1)), size = e & 0x7FFFu;
+        if (size < least) continue;
+        const int code = (int)(word >> (4 * ((i >> 1) + 4 * (i & 1))) & 15u);
+        sum += (float)(code - zero) * scale * (size > nan ? NAN : e & 0x8000u ? -INFINITY : INFINITY);
+    }
 }
 
-// x: the token's row of K bf16.
+// x: the token's row of K bf16 (K a multiple of 8).
 __device__ __noinline__ float ft_resolve(const uint8_t *chunk, uint32_t step, uint32_t where, const __nv_bfloat16 *x, int K,
                                          float v)
 {
     float sum = 0.0f;
-    bool found = false;
 #pragma unroll 1
-    for (int k = 0; k < K; ++k) {
-        if ((k & 7) == 0) {   // eight at once: none?
-            const uint4 u = *reinterpret_cast<const uint4 *>(x + k);
-            auto any = [](uint32_t w) { return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u; };
-            if (!any(u.x) && !any(u.y) && !any(u.z) && !any(u.w)) {
-                k += 7;
-                continue;
-            }
-        }
-        const uint32_t e = __bfloat16_as_ushort(x[k]);
-        if ((e & 0x7FFFu) < 0x7F80u) continue;
-        sum += ft_weight(chunk + (int64_t)(k >> 8) * step, where, k) * __uint_as_float(e << 16);
-        found = true;
+    for (int k = 0; k < K; k += 8) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(x + k);
+        auto any = [](uint32_t w) { return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u; };
+        if (!any(u.x) && !any(u.y) && !any(u.z) && !any(u.w)) continue;
+        ft_add_special(chunk, step, where, k, u, 0x7F80u, 0x7F80u, sum);
         if (sum != sum) break;
     }
-    return found ? sum : v;
+    return sum != 0.0f ? sum : v;   // (an infinity or NaN, once there is one)
 }
 
 // --- bf16 weights ----------------------------------------------------------------

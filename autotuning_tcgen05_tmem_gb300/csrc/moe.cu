@@ -433,14 +433,13 @@ __device__ __noinline__ float ft_resolve_h(const uint8_t *chunk, uint32_t step, 
 {
     float sum = 0.0f;
 #pragma unroll 1
-    for (int k = 0; k < I; ++k) {
-        if (__ldcg(powers + ((int64_t)(k >> 8) * rows * 4 + (k >> 6 & 3))) != INFINITY) {
-            k |= 63;
+    for (int k = 0; k < I; k += 8) {
+        if ((k & 63) == 0 && __ldcg(powers + ((int64_t)(k >> 8) * rows * 4 + (k >> 6 & 3))) != INFINITY) {
+            k += 56;
             continue;
         }
-        const float mark = __half2float(__ldcg(h + ((int64_t)(k >> 8) * rows * kWqChunkK + (k & 255))));
-        if (mark == 0.0f) continue;
-        sum += ft_weight(chunk + (int64_t)(k >> 8) * step, where, k) * (mark != mark ? mark : mark * INFINITY);
+        const uint4 u = __ldcg(reinterpret_cast<const uint4 *>(h + ((int64_t)(k >> 8) * rows * kWqChunkK + (k & 255))));
+        ft_add_special(chunk, step, where, k, u, 1u, 0x7C00u, sum);
         if (sum != sum) break;
     }
     return sum;
